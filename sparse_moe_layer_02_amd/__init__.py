@@ -72,7 +72,7 @@ def lib():
                 raise RuntimeError(f"{LIB_PATH} is missing: build it first "
                                    "(python -c 'import __graft_entry__ as g; g.build()')")
             l = ctypes.CDLL(LIB_PATH)
-            for name, (args, res) in _SIGS.items():
+            for name, (args, res) in (*_SIGS.items(), *_block.SIGS.items()):
                 f = getattr(l, name)
                 f.argtypes = args
                 f.restype = res
@@ -434,10 +434,19 @@ def moe_profile_summary() -> dict:
     return out
 
 
+# ----------------------------------- 4-bit expert weights and block norms --
+
+from . import block as _block  # noqa: E402
+from .block import (MXFP4, block_forward, moe_expert_ffn_mxfp4,  # noqa: E402,F401
+                    moe_expert_ffn_mxfp4_workspace_bytes, moe_grouped_gemm_mxfp4,
+                    moe_grouped_gemm_mxfp4_workspace_bytes, moe_mxfp4_dequantize,
+                    moe_mxfp4_quantize, moe_norm, moe_norm_residual, quantize_weights)
+
+
 # ------------------------------------------------------- buffers + forward --
 
 def alloc_buffers(T, H, E, n_ffn, I, K, dtype, device="cuda", grouped_copy=False,
-                  separate_identity=False):
+                  separate_identity=False, mxfp4=False, residual=None):
     """Device buffers for one forward pass (torch allocations; no compute).
     grouped_copy: also allocate x_perm [T*K, H], and forward() then copies the
     grouped rows (moe_permute + moe_expert_ffn); by default the expert GEMM
@@ -445,8 +454,19 @@ def alloc_buffers(T, H, E, n_ffn, I, K, dtype, device="cuda", grouped_copy=False
     separate_identity: also allocate y_acc [T, H] fp32, and forward() runs the
     identity experts as their own call (moe_zero_experts, then moe_combine);
     by default combine computes their term itself (moe_combine_identity) and
-    y_acc is None.  Both options give bitwise the same y."""
+    y_acc is None.  Both options give bitwise the same y.
+    mxfp4: size the expert workspace for MXFP4 expert weights too.
+    residual: the dtype of a residual stream around the layer, for
+    block_forward(): also allocate x_norm and h_norm [T, H] in dtype and h_out
+    [T, H] in residual."""
     rows = T * K
+    ws_bytes = max(256, moe_expert_ffn_workspace_bytes(rows, n_ffn, I, dtype))
+    if mxfp4:
+        ws_bytes = max(ws_bytes, moe_expert_ffn_mxfp4_workspace_bytes(rows, n_ffn, I))
+    block = {} if residual is None else dict(
+        x_norm=torch.empty((T, H), dtype=dtype, device=device),
+        h_norm=torch.empty((T, H), dtype=dtype, device=device),
+        h_out=torch.empty((T, H), dtype=residual, device=device))
     f32, i32 = torch.float32, torch.int32
     return dict(
         logits=torch.empty((T, E), dtype=f32, device=device),
@@ -459,8 +479,7 @@ def alloc_buffers(T, H, E, n_ffn, I, K, dtype, device="cuda", grouped_copy=False
         row_src=torch.empty((rows,), dtype=i32, device=device),
         slot_row=torch.empty((rows,), dtype=i32, device=device),
         y_perm=torch.empty((rows, H), dtype=dtype, device=device),
-        ws_ffn=torch.empty((max(256, moe_expert_ffn_workspace_bytes(rows, n_ffn, I, dtype)),),
-                           dtype=torch.uint8, device=device),
+        ws_ffn=torch.empty((ws_bytes,), dtype=torch.uint8, device=device),
         y_acc=torch.empty((T, H), dtype=f32, device=device) if separate_identity else None,
         y=torch.empty((T, H), dtype=dtype, device=device),
         w_planes=None,   # the router weights' planes, set by prepare_router()
@@ -469,6 +488,7 @@ def alloc_buffers(T, H, E, n_ffn, I, K, dtype, device="cuda", grouped_copy=False
         side_stream=torch.cuda.Stream(device=device) if separate_identity else None,
         ev_routed=torch.cuda.Event() if separate_identity else None,
         ev_identity=torch.cuda.Event() if separate_identity else None,
+        **block,
     )
 
 
@@ -480,7 +500,10 @@ def forward(x, w_router, bias, w13, w2, K, ffn_scale, buf):
     With the default buffers: router, routing, dispatch (indices only), the
     expert GEMMs gathering their rows from x, and combine with the identity
     experts' term folded in -- five calls.  With separate_identity buffers,
-    the six calls of _forward_six."""
+    the six calls of _forward_six.
+    w13 and w2 may be MXFP4 (quantize_weights), with bf16 tokens and buffers of
+    alloc_buffers(..., mxfp4=True): the experts then run on 4-bit weights
+    (moe_expert_ffn_mxfp4)."""
     if buf["y_acc"] is None:
         return _forward_fused(x, w_router, bias, w13, w2, K, ffn_scale, buf)
     return _forward_six(x, w_router, bias, w13, w2, K, ffn_scale, buf)
@@ -529,8 +552,14 @@ def _forward_six(x, w_router, bias, w13, w2, K, ffn_scale, buf):
 def _dispatch_and_experts(x, K, n_ffn, w13, w2, buf):
     """Dispatch and the FFN experts.  Without an x_perm buffer, dispatch
     writes only the indices and the first expert GEMM loads each grouped row
-    straight from x (0.9 GB less HBM traffic on the 8192-token layer)."""
-    if buf["x_perm"] is None:
+    straight from x (0.9 GB less HBM traffic on the 8192-token layer).  On
+    MXFP4 weights the rows are always gathered."""
+    if isinstance(w13, MXFP4):
+        moe_permute(x, buf["topk_idx"], buf["counts"], n_ffn, buf["offsets"], None,
+                    buf["row_src"], buf["slot_row"])
+        moe_expert_ffn_mxfp4(x, None, K, buf["row_src"], buf["offsets"], *w13, *w2,
+                             buf["y_perm"], buf["ws_ffn"])
+    elif buf["x_perm"] is None:
         moe_permute(x, buf["topk_idx"], buf["counts"], n_ffn, buf["offsets"], None,
                     buf["row_src"], buf["slot_row"])
         moe_expert_ffn_gather(x, K, buf["row_src"], buf["offsets"], w13, w2, buf["y_perm"],

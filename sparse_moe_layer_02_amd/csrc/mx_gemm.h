@@ -1,0 +1,490 @@
+// Matrix products grouped by expert on microscaled 4-bit weights (MXFP4: e2m1
+// codes, one e8m0 scale per 32 values of a row), for rows in bf16 or in MXFP4.
+//
+//   out[r][n] = sum_d a(r)[d] * w_e[n][d],  r in expert e's span of offsets
+//
+// What bounds it.  Up to ~250 rows an expert the weights' 17/32 byte a value,
+// past that the matrix cores (bf16 rows: from ~100 rows on).  So one block
+// takes up to 256 rows of one expert, and a weight byte is loaded once:
+//   - a wave owns 16 CB weight rows and every row of the tile, so no two waves
+//     load the same weights and they go from memory straight to registers, one
+//     512-value chunk of each row ahead of its use (J = 4 slices of 128);
+//   - rows are the second operand, weights the first: a lane then holds 4
+//     consecutive output columns of one row per 16 x 16 block, and the weight
+//     rows are dealt to the CB blocks so that its 4 CB columns are consecutive
+//     and go out as 16-byte stores, a whole 128-byte line per row and wave;
+//   - the rows go through LDS, in tiles of 256 bytes a row (512 4-bit values
+//     or 128 bf16), two stages, the 16-byte chunks XOR-swizzled by the row.
+// MXFP4 rows: v_mfma_scale_f32_16x16x128_f8f6f4, both scales applied by the
+// instruction (lane l holds row l % 16, values 32 (l / 16) + [0, 32): one scale
+// block).  bf16 rows: the 32 codes of a lane become four 8-value fragments of
+// v_mfma_f32_16x16x32_bf16 (exact: e2m1 times a power of two has two
+// significant bits), the activation fragment taken at the same values.
+// Sums are fp32 in both.
+//
+// A row length that is no multiple of 512 ends with the chunk [D - 512, D)
+// whose part before the last whole multiple is skipped (bf16 rows) or meets
+// zero codes (MXFP4 rows): every weight load stays a full one inside its row.
+#pragma once
+
+#include <type_traits>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace mx {
+
+typedef __attribute__((__vector_size__(8 * sizeof(int)))) int i32x8;
+typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+// a 16-byte load at a 4-byte aligned address (scale rows)
+typedef i32x4 __attribute__((aligned(4))) i32x4u;
+
+constexpr int kThreads = 256;      // 4 waves
+constexpr int kPitch = 256;        // bytes of a row in an LDS stage
+constexpr int kChunk = 512;        // values of a weight row per load chunk
+constexpr int kMaxRows = 256;      // rows of an m-tile
+constexpr int kSmallRows = 32;     // m-tiles of the small-batch kernels
+constexpr int kFp4 = 4;            // the instruction's operand format code for e2m1
+
+struct GemmArgs {
+  const void* a;                   // bf16 [.][D] or codes [.][D / 2]
+  const uint8_t* a_scales;         // [.][D / 32], MXFP4 rows only
+  const int32_t* row_src;          // row r reads a[row_src[r] / K]; NULL: a[r]
+  int K, T;
+  const int32_t* offsets;
+  int rows_cap, n_experts, D, N;
+  const uint8_t* w;                // [E][N][D / 2]
+  const uint8_t* w_scales;         // [E][N][D / 32]
+  void* out;                       // [.][N] or, SwiGLU, [.][N / 2]
+  // list mode: tiles[first .. first + *count); direct mode (count NULL): the
+  // m-tile is expert number
+  const int4* tiles;
+  const int* first;
+  const int* count;
+  int NT;                          // column tiles
+};
+
+__device__ __forceinline__ int swz16(int row, int chunk) { return chunk ^ (row & 15); }
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+template <typename OutT, int C>
+__device__ __forceinline__ void store_cols(OutT* o, const float* v) {
+  if constexpr (sizeof(OutT) == 2) {
+    if constexpr (C % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < C; i += 8) {
+        bf16x8 p;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = (bf16)v[i + k];
+        *(bf16x8*)(o + i) = p;
+      }
+    } else {
+      typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
+      bf16x4 p;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = (bf16)v[k];
+      *(bf16x4*)o = p;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; i += 4) *(f32x4*)(o + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  }
+}
+
+// LDS of a tile of 16 R rows: two stages of rows, and for MXFP4 rows two
+// stages of their scales (one dword a row and 32-value group of a slice: byte
+// j is slice j's).
+template <int R, bool A4>
+constexpr int lds_bytes() {
+  return 2 * 16 * R * kPitch + (A4 ? 2 * 16 * R * 16 : 0);
+}
+
+template <int R, int CB, bool A4, bool SW, typename OutT>
+__device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int row0, int rows,
+                                     int nt) {
+  static_assert(!SW || CB % 2 == 0, "gate and up blocks come in pairs");
+  constexpr int CBH = SW ? CB / 2 : CB;         // blocks of output columns
+  constexpr int BM = 16 * R;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int m = lane & 15, g = lane >> 4;
+  const int D = p.D, N = p.N;
+  const int width = SW ? N / 2 : N;             // output columns
+  const int code_pitch = D >> 1, scale_pitch = D >> 5;
+  const bool small = D < kChunk;                // one chunk, shorter than 512
+  const int KC = (D + kChunk - 1) / kChunk;
+  // first value of chunk c
+  auto window = [&](int c) { return small ? 0 : min(c * kChunk, D - kChunk); };
+
+  // ---- weights: lane l of block cb holds weight row (cb, l % 16), group g
+  const int col0 = nt * (64 * CBH) + wave * (16 * CBH);   // first output column of the wave
+  const char* wbase = (const char*)p.w + (size_t)e * N * code_pitch;
+  const char* sbase = (const char*)p.w_scales + (size_t)e * N * scale_pitch;
+  uint32_t woff[CB], soff[CB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb) {
+    const int h = cb % CBH;
+    const int j = min(col0 + (m >> 2) * (4 * CBH) + 4 * h + (m & 3), width - 1);
+    const uint32_t n = (uint32_t)(j + (SW && cb >= CBH ? width : 0));
+    woff[cb] = n * (uint32_t)code_pitch + 16u * g;
+    soff[cb] = n * (uint32_t)scale_pitch;
+  }
+  auto load_scales = [&](const char* s, int k0) -> i32x4 {
+    if (!small) return *(const i32x4u*)(s + (k0 >> 5));
+    i32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *(const int*)(s + min(4 * j, scale_pitch - 4));
+    return v;
+  };
+
+  // ---- rows: thread t stages 16-byte chunk t % 16 of rows t / 16 + 16 i
+  const int sr = tid >> 4, sc = tid & 15;
+  const int a_pitch = A4 ? code_pitch : 2 * D;
+  auto source_row = [&](int r) -> size_t {
+    const int q = row0 + min(r, rows - 1);
+    return p.row_src ? (size_t)min(max(p.row_src[q], 0) / p.K, p.T - 1) : (size_t)q;
+  };
+  const char* arow[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    arow[i] = (const char*)p.a + source_row(sr + 16 * i) * a_pitch;
+
+  f32x4 acc[R][CB];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  const int stage_bytes = BM * kPitch;
+  auto write_rows = [&](char* st, const i32x4* v) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = sr + 16 * i;
+      *(i32x4*)(st + r * kPitch + swz16(r, sc) * 16) = v[i];
+    }
+  };
+  auto frag = [&](const char* st, int rb, int chunk) {
+    const int r = 16 * rb + m;
+    return *(const i32x4*)(st + r * kPitch + swz16(r, chunk) * 16);
+  };
+
+  if constexpr (A4) {
+    char* scl = smem + 2 * stage_bytes;
+    const char* asrow =
+        (const char*)p.a_scales + (tid < BM ? source_row(tid) : 0) * (size_t)scale_pitch;
+    i32x4 av[R], as;
+    i32x4 wq[2][CB][4], ws[2][CB];
+    // byte g of dwords 0..3 of v, as one dword
+    const int sel = g | ((4 + g) << 8) | 0x0c0c0000;
+    auto pick = [&](const i32x4& v, int s) {
+      const int lo = __builtin_amdgcn_perm(v[1], v[0], s), hi = __builtin_amdgcn_perm(v[3], v[2], s);
+      return (int)__builtin_amdgcn_perm(hi, lo, 0x05040100);
+    };
+    auto load_a = [&](int c) {
+      const int k0 = window(c);
+      // values before c * 512 were multiplied in the chunk before, values
+      // past D do not exist: zero codes
+      const int k = k0 + 32 * sc;
+      const bool live = k >= c * kChunk && k < D;
+      const int kb = small ? min(16 * sc, code_pitch - 16) : (k0 >> 1) + 16 * sc;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        i32x4 v = *(const i32x4*)(arow[i] + kb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) av[i][q] = live ? v[q] : 0;
+      }
+      if (tid < BM) as = load_scales(asrow, k0);
+    };
+    auto write_a = [&](int b) {
+      write_rows(smem + b * stage_bytes, av);
+      if (tid < BM) {
+        i32x4 t;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) t[q] = pick(as, q | ((4 + q) << 8) | 0x0c0c0000);
+        *(i32x4*)(scl + (b * BM + tid) * 16) = t;
+      }
+    };
+    auto load_w = [&](auto B, int c) {
+      constexpr int b = decltype(B)::value;
+      const int k0 = window(c);
+      const char* wc = wbase + (k0 >> 1);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          wq[b][cb][j] =
+              *(const i32x4*)(wc + woff[cb] + (small ? min(64 * j, code_pitch - 64) : 64 * j));
+        ws[b][cb] = load_scales(sbase + soff[cb], k0);
+      }
+    };
+    auto compute = [&](auto B) {
+      constexpr int b = decltype(B)::value;
+      const char* st = smem + b * stage_bytes;
+      int sa[R], sw[CB];
+#pragma unroll
+      for (int rb = 0; rb < R; ++rb)
+        sa[rb] = *(const int*)(scl + (b * BM + 16 * rb + m) * 16 + 4 * g);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) sw[cb] = pick(ws[b][cb], sel);
+#define MX_SLICE(J)                                                                              \
+  _Pragma("unroll") for (int rb = 0; rb < R; ++rb) {                                             \
+    const i32x4 f = frag(st, rb, 4 * J + g);                                                     \
+    const i32x8 fa = {f[0], f[1], f[2], f[3], 0, 0, 0, 0};                                       \
+    _Pragma("unroll") for (int cb = 0; cb < CB; ++cb) {                                          \
+      const i32x4 w = wq[b][cb][J];                                                              \
+      const i32x8 fw = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};                                     \
+      acc[rb][cb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                            \
+          fw, fa, acc[rb][cb], kFp4, kFp4, J, sw[cb], J, sa[rb]);                                \
+    }                                                                                            \
+  }
+      MX_SLICE(0)
+      MX_SLICE(1)
+      MX_SLICE(2)
+      MX_SLICE(3)
+#undef MX_SLICE
+    };
+    std::integral_constant<int, 0> P0;
+    std::integral_constant<int, 1> P1;
+    load_a(0);
+    load_w(P0, 0);
+    write_a(0);
+    lds_barrier();
+    auto step = [&](auto cur, auto nxt, int c) {
+      const bool more = c + 1 < KC;
+      if (more) {
+        load_a(c + 1);      // before the weights: the wait for it leaves them in flight
+        load_w(nxt, c + 1);
+      }
+      compute(cur);
+      if (more) write_a(decltype(nxt)::value);
+      lds_barrier();
+    };
+    for (int c = 0; c < KC; c += 2) {
+      step(P0, P1, c);
+      if (c + 1 < KC) step(P1, P0, c + 1);
+    }
+  } else {
+    constexpr int PA = R <= 4 ? 4 : R <= 8 ? 2 : 1;   // row stages in flight in registers
+    i32x4 av[PA][R];
+    i32x4 wq[4][CB], ws[CB], wn[CB];
+    const int S = 4 * KC;
+    auto load_a = [&](i32x4* v, int s) {
+      const int k = window(s >> 2) + 128 * (s & 3);
+      const int kb = 2 * min(k, D - 128) + 16 * sc;
+#pragma unroll
+      for (int i = 0; i < R; ++i) v[i] = *(const i32x4*)(arow[i] + kb);
+    };
+    auto load_w = [&](auto J, int c) {
+      constexpr int j = decltype(J)::value;
+      const char* wc = wbase + (window(c) >> 1);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        wq[j][cb] =
+            *(const i32x4*)(wc + woff[cb] + (small ? min(64 * j, code_pitch - 64) : 64 * j));
+    };
+    auto compute = [&](auto J, int b) {
+      constexpr int j = decltype(J)::value;
+      const char* st = smem + b * stage_bytes;
+      bf16x8 fw[CB][4];
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        // e8m0 byte as an fp32 power of two (0xFF: NaN)
+        const float sc2 = __uint_as_float(__builtin_amdgcn_ubfe((unsigned)ws[cb][j], 8 * g, 8) << 23);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const unsigned u = (unsigned)wq[j][cb][q];
+          const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 0);
+          const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 1);
+          const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 2);
+          const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 3);
+          fw[cb][q] = bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int rb = 0; rb < R; ++rb) {
+          const bf16x8 fa = __builtin_bit_cast(bf16x8, frag(st, rb, 4 * g + q));
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb)
+            acc[rb][cb] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[cb][q], fa, acc[rb][cb], 0, 0, 0);
+        }
+    };
+    auto each4 = [&](auto&& f) {
+      f(std::integral_constant<int, 0>{});
+      f(std::integral_constant<int, 1>{});
+      f(std::integral_constant<int, 2>{});
+      f(std::integral_constant<int, 3>{});
+    };
+    // stage s's rows, then stages 1 .. PA in registers, chunk 0's weights
+    load_a(av[0], 0);
+    {
+      write_rows(smem, av[0]);
+    }
+#pragma unroll
+    for (int i = 1; i <= PA; ++i) load_a(av[i % PA], min(i, S - 1));
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) ws[cb] = load_scales(sbase + soff[cb], 0);
+    each4([&](auto J) { load_w(J, 0); });
+    lds_barrier();
+    for (int c = 0; c < KC; ++c) {
+      const bool more = c + 1 < KC;
+      const int k0 = window(c);
+      each4([&](auto J) {
+        constexpr int j = decltype(J)::value;
+        const int s = 4 * c + j;
+        if (s + 1 < S) {
+          i32x4* v = av[(j + 1) % PA];
+          write_rows(smem + ((j + 1) & 1) * stage_bytes, v);
+          load_a(v, min(s + 1 + PA, S - 1));
+        }
+        const int k = k0 + 128 * j;
+        if (k >= c * kChunk && k < D) compute(J, j & 1);
+        if (more) {
+          if (j == 0) {
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+              wn[cb] = load_scales(sbase + soff[cb], window(c + 1));
+          }
+          load_w(J, c + 1);
+        }
+        lds_barrier();
+      });
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) ws[cb] = wn[cb];
+    }
+  }
+
+  // ---- lane l: row 16 rb + l % 16, output columns col0 + 4 CBH g + [0, 4 CBH)
+  const int n0 = col0 + 4 * CBH * g;
+  if (n0 >= width) return;
+#pragma unroll
+  for (int rb = 0; rb < R; ++rb) {
+    const int r = 16 * rb + m;
+    if (r >= rows) continue;
+    float v[4 * CBH];
+#pragma unroll
+    for (int h = 0; h < CBH; ++h)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[4 * h + q] = SW ? silu(acc[rb][h][q]) * acc[rb][CBH + (SW ? h : 0) - (SW ? 0 : CBH)][q]
+                          : acc[rb][h][q];
+    store_cols<OutT, 4 * CBH>((OutT*)p.out + (size_t)(row0 + r) * width + n0, v);
+  }
+}
+
+// Block -> (m-tile, column tile).  Consecutive blocks land on the 8 XCDs in
+// turn, so all column tiles of one m-tile run on one XCD and share its rows in
+// that XCD's L2.
+__device__ __forceinline__ bool find_tile(const GemmArgs& p, int4& t, int& nt) {
+  const int b = blockIdx.x, slot = b >> 3;
+  const int mt = (slot / p.NT) * 8 + (b & 7);
+  nt = slot % p.NT;
+  if (p.count) {
+    if (mt >= *p.count) return false;
+    t = p.tiles[*p.first + mt];
+    return true;
+  }
+  if (mt >= p.n_experts) return false;
+  const int r0 = min(max(p.offsets[mt], 0), p.rows_cap);
+  const int n = min(max(p.offsets[mt + 1], r0), p.rows_cap) - r0;
+  t = make_int4(mt, r0, n, 1);
+  return n > 0;
+}
+
+// m-tiles of at most 32 rows.  Direct mode is taken where no dispatch gives an
+// expert more; one that has more all the same is taken 32 rows at a time.
+template <int CB, bool A4, bool SW, typename OutT>
+__global__ __launch_bounds__(kThreads, 2) void gemm_small(GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<2, A4>()];
+  int4 t;
+  int nt;
+  if (!find_tile(p, t, nt)) return;
+  for (int r = 0; r < t.z; r += kSmallRows) {
+    const int rows = min(kSmallRows, t.z - r);
+    if (rows <= 16)
+      tile<1, CB, A4, SW, OutT>(smem, p, t.x, t.y + r, rows, nt);
+    else
+      tile<2, CB, A4, SW, OutT>(smem, p, t.x, t.y + r, rows, nt);
+  }
+}
+
+// m-tiles of up to 256 rows
+template <bool A4, bool SW, typename OutT>
+__global__ __launch_bounds__(kThreads, 1) void gemm_large(GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<16, A4>()];
+  int4 t;
+  int nt;
+  if (!find_tile(p, t, nt)) return;
+  if (t.z <= 64)
+    tile<4, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if (t.z <= 128)
+    tile<8, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if (t.z <= 192)
+    tile<12, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else
+    tile<16, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+}
+
+// cb: column blocks per wave of the small kernel (4, 2, and without SwiGLU 1)
+template <bool A4>
+hipError_t launch_gemm_small(GemmArgs p, bool swiglu, int out_dtype, int cb, unsigned mtiles,
+                             hipStream_t s);
+template <bool A4>
+hipError_t launch_gemm_large(GemmArgs p, bool swiglu, int out_dtype, unsigned mtiles,
+                             hipStream_t s);
+
+template <bool A4>
+struct Launch {
+  template <int CB, bool SW, typename OutT>
+  static void small(GemmArgs& p, unsigned mtiles, hipStream_t s) {
+    const int width = SW ? p.N / 2 : p.N;
+    p.NT = (int)ceil_div(width, SW ? 32 * CB : 64 * CB);
+    const unsigned grid = ceil_div(mtiles, 8) * 8 * p.NT;
+    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
+               gemm_small<CB, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  }
+  template <bool SW, typename OutT>
+  static void small_cb(GemmArgs& p, int cb, unsigned mtiles, hipStream_t s) {
+    if (cb >= 4) return small<4, SW, OutT>(p, mtiles, s);
+    if constexpr (!SW) {
+      if (cb == 1) return small<1, SW, OutT>(p, mtiles, s);
+    }
+    return small<2, SW, OutT>(p, mtiles, s);
+  }
+  template <bool SW, typename OutT>
+  static void large(GemmArgs& p, unsigned mtiles, hipStream_t s) {
+    const int width = SW ? p.N / 2 : p.N;
+    p.NT = (int)ceil_div(width, SW ? 128 : 256);
+    const unsigned grid = ceil_div(mtiles, 8) * 8 * p.NT;
+    MOE_LAUNCH(A4 ? "mx_gemm_large_fp4" : "mx_gemm_large_bf16", s,
+               gemm_large<A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  }
+};
+
+#define MX_INSTANTIATE(A4)                                                                       \
+  template <>                                                                                    \
+  hipError_t launch_gemm_small<A4>(GemmArgs p, bool swiglu, int out_dtype, int cb,               \
+                                   unsigned mtiles, hipStream_t s) {                             \
+    if (out_dtype == MOE_BF16)                                                                   \
+      swiglu ? Launch<A4>::small_cb<true, bf16>(p, cb, mtiles, s)                                \
+             : Launch<A4>::small_cb<false, bf16>(p, cb, mtiles, s);                              \
+    else                                                                                         \
+      swiglu ? Launch<A4>::small_cb<true, float>(p, cb, mtiles, s)                               \
+             : Launch<A4>::small_cb<false, float>(p, cb, mtiles, s);                             \
+    return hipGetLastError();                                                                    \
+  }                                                                                              \
+  template <>                                                                                    \
+  hipError_t launch_gemm_large<A4>(GemmArgs p, bool swiglu, int out_dtype, unsigned mtiles,      \
+                                   hipStream_t s) {                                              \
+    if (out_dtype == MOE_BF16)                                                                   \
+      swiglu ? Launch<A4>::large<true, bf16>(p, mtiles, s)                                       \
+             : Launch<A4>::large<false, bf16>(p, mtiles, s);                                     \
+    else                                                                                         \
+      swiglu ? Launch<A4>::large<true, float>(p, mtiles, s)                                      \
+             : Launch<A4>::large<false, float>(p, mtiles, s);                                    \
+    return hipGetLastError();                                                                    \
+  }
+
+}  // namespace mx
+}  // namespace moe

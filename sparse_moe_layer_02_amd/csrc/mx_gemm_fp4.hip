@@ -1,0 +1,8 @@
+// Grouped products of MXFP4 rows on MXFP4 weights (the kernels are in mx_gemm.h).
+#include "mx_gemm.h"
+
+namespace moe {
+namespace mx {
+MX_INSTANTIATE(true)
+}  // namespace mx
+}  // namespace moe
