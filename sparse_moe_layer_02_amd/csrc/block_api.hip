@@ -109,7 +109,7 @@ moe_status moe_grouped_gemm_mxfp4(const void* a, const uint8_t* a_scales, const 
   if (n_experts == 0) return MOE_OK;
   const hipStream_t s = (hipStream_t)stream;
   const int most = rows_max(row_src, rows_cap, T);
-  hipError_t e = mx::launch_tiles(offsets, rows_cap, n_experts, most, ws, s);
+  hipError_t e = mx::launch_tiles(offsets, rows_cap, n_experts, most, a_scales != nullptr, ws, s);
   if (e == hipSuccess)
     e = mx::launch_product(a, a_scales, row_src, T, K, offsets, rows_cap, n_experts, most, D, N, w,
                            w_scales, swiglu != 0, out_dtype, out, ws, s);
@@ -143,7 +143,7 @@ moe_status moe_expert_ffn_mxfp4(const void* x, const uint8_t* x_scales, int T, i
   if (n_ffn == 0) return MOE_OK;
   const hipStream_t s = (hipStream_t)stream;
   const int most = rows_max(row_src, rows_cap, T);
-  hipError_t e = mx::launch_tiles(offsets, rows_cap, n_ffn, most, f.list, s);
+  hipError_t e = mx::launch_tiles(offsets, rows_cap, n_ffn, most, x_scales != nullptr, f.list, s);
   if (e == hipSuccess)
     e = mx::launch_product(x, x_scales, row_src, T, K, offsets, rows_cap, n_ffn, most, H, 2 * I,
                            w13, w13_scales, true, MOE_BF16, f.hh, f.list, s);

@@ -19,9 +19,9 @@ size_t tile_list_bytes(int rows_cap, int n_experts);
 // Whether the products fit the launch limits (blocks of a grid).
 bool grid_fits(int rows_cap, int n_experts, int N);
 // rows_max: upper bound of an expert's rows.  list: the m-tile list is filled
-// by launch_tiles for the same offsets, rows_cap and rows_max.
+// by launch_tiles for the same offsets, rows_cap, rows_max and form of rows.
 hipError_t launch_tiles(const int32_t* offsets, int rows_cap, int n_experts, int rows_max,
-                        void* ws, hipStream_t s);
+                        bool fp4_rows, void* ws, hipStream_t s);
 hipError_t launch_product(const void* a, const uint8_t* a_scales, const int32_t* row_src, int T,
                           int K, const int32_t* offsets, int rows_cap, int n_experts, int rows_max,
                           int D, int N, const uint8_t* w, const uint8_t* w_scales, bool swiglu,

@@ -42,8 +42,14 @@ typedef i32x4 __attribute__((aligned(4))) i32x4u;
 constexpr int kThreads = 256;      // 4 waves
 constexpr int kPitch = 256;        // bytes of a row in an LDS stage
 constexpr int kChunk = 512;        // values of a weight row per load chunk
-constexpr int kMaxRows = 256;      // rows of an m-tile
+// Rows of an m-tile.  MXFP4 rows: one tile for nearly every expert that the
+// weights bound (its weights are loaded once).  bf16 rows: the matrix cores
+// bound an expert of more than about 100 rows, and 256 rows' accumulators next
+// to the fragments in two forms do not fit the registers.
+template <bool A4> constexpr int kMaxRows = A4 ? 256 : 128;
 constexpr int kSmallRows = 32;     // m-tiles of the small-batch kernels
+using Yes = std::true_type;
+using No = std::false_type;
 constexpr int kFp4 = 4;            // the instruction's operand format code for e2m1
 
 struct GemmArgs {
@@ -116,6 +122,13 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   // first value of chunk c
   auto window = [&](int c) { return small ? 0 : min(c * kChunk, D - kChunk); };
 
+  auto each4 = [&](auto&& f) {
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
+  };
+
   // ---- weights: lane l of block cb holds weight row (cb, l % 16), group g
   const int col0 = nt * (64 * CBH) + wave * (16 * CBH);   // first output column of the wave
   const char* wbase = (const char*)p.w + (size_t)e * N * code_pitch;
@@ -129,32 +142,64 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     woff[cb] = n * (uint32_t)code_pitch + 16u * g;
     soff[cb] = n * (uint32_t)scale_pitch;
   }
-  auto load_scales = [&](const char* s, int k0) -> i32x4 {
-    if (!small) return *(const i32x4u*)(s + (k0 >> 5));
+  // Loads of chunk 0 also take rows shorter than a chunk (FIRST): the same
+  // places again instead of bytes past the row.  Loads inside the loop do not
+  // branch, so that the waits for them stay exact.
+  const int short_j = small ? scale_pitch / 4 - 1 : 3;    // last slice of a short row
+  auto load_scales = [&](auto FIRST, const char* s, int k0) -> i32x4 {
+    if constexpr (!decltype(FIRST)::value) return *(const i32x4u*)(s + (k0 >> 5));
     i32x4 v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *(const int*)(s + min(4 * j, scale_pitch - 4));
+    for (int j = 0; j < 4; ++j) v[j] = *(const int*)(s + 4 * min(j, short_j));
     return v;
   };
+  auto load_codes = [&](auto FIRST, const char* w, int j) {
+    return *(const i32x4*)(w + (decltype(FIRST)::value ? 64 * min(j, short_j) : 64 * j));
+  };
 
-  // ---- rows: thread t stages 16-byte chunk t % 16 of rows t / 16 + 16 i
+  i32x4 wq[4][CB], wn[CB];                      // a chunk's codes; the next chunk's scales
+  auto load_w = [&](auto FIRST, auto J, int c) {
+    constexpr int j = decltype(J)::value;
+    const char* wc = wbase + (window(c) >> 1);
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) wq[j][cb] = load_codes(FIRST, wc + woff[cb], j);
+  };
+  auto load_ws = [&](auto FIRST, int c) {
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) wn[cb] = load_scales(FIRST, sbase + soff[cb], window(c));
+  };
+
+  // ---- rows: thread t stages 16-byte chunk t % 16 of rows t / 16 + 16 i;
+  // rows past the tile's are its last one again (never stored)
   const int sr = tid >> 4, sc = tid & 15;
   const int a_pitch = A4 ? code_pitch : 2 * D;
-  auto source_row = [&](int r) -> size_t {
-    const int q = row0 + min(r, rows - 1);
-    return p.row_src ? (size_t)min(max(p.row_src[q], 0) / p.K, p.T - 1) : (size_t)q;
-  };
-  const char* arow[R];
+  constexpr int NQ = A4 ? R + 1 : R;
+  int src[NQ];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    arow[i] = (const char*)p.a + source_row(sr + 16 * i) * a_pitch;
+  for (int i = 0; i < NQ; ++i)
+    src[i] = row0 + min(i < R ? sr + 16 * i : min(tid, BM - 1), rows - 1);
+  if (p.row_src) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) src[i] = p.row_src[src[i]];
+  }
+  // chunk 0's weights are on their way while the row indices arrive
+  load_ws(Yes{}, 0);
+  each4([&](auto J) { load_w(Yes{}, J, 0); });
+  if (p.row_src) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) src[i] = min(max(src[i], 0) / p.K, p.T - 1);
+  }
+  uint32_t arow[R];                              // in 16-byte units from a
+#pragma unroll
+  for (int i = 0; i < R; ++i) arow[i] = (uint32_t)(((size_t)src[i] * a_pitch) >> 4);
+  auto row_ptr = [&](int i) { return (const char*)p.a + ((size_t)arow[i] << 4); };
 
   f32x4 acc[R][CB];
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < CB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  const int stage_bytes = BM * kPitch;
+  constexpr int stage_bytes = BM * kPitch;
   auto write_rows = [&](char* st, const i32x4* v) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -166,193 +211,195 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     const int r = 16 * rb + m;
     return *(const i32x4*)(st + r * kPitch + swz16(r, chunk) * 16);
   };
+  // A chunk runs as groups of RG row blocks (RG * CB matrix instructions); the
+  // fragments of a group are read from LDS before the group in front of it is
+  // multiplied.  Each group is a basic block of its own, behind a branch on a
+  // value the compiler cannot see through: matrix instructions have no side
+  // effects, and without the branches they are all moved behind the waits for
+  // the next chunk's loads, which then hide behind nothing.
+  constexpr int RG = R < 4 ? R : 4;
+  constexpr int NH = R / RG;                     // groups per slice
+  static_assert(R % RG == 0, "whole groups");
+  i32x4 fr[2][RG];
+  auto opaque = [&] {
+    int one = 1;
+    asm volatile("" : "+s"(one));
+    return one != 0;
+  };
 
   if constexpr (A4) {
     char* scl = smem + 2 * stage_bytes;
-    const char* asrow =
-        (const char*)p.a_scales + (tid < BM ? source_row(tid) : 0) * (size_t)scale_pitch;
+    const char* as_ptr = (const char*)p.a_scales + (size_t)src[R] * scale_pitch;
     i32x4 av[R], as;
-    i32x4 wq[2][CB][4], ws[2][CB];
-    // byte g of dwords 0..3 of v, as one dword
-    const int sel = g | ((4 + g) << 8) | 0x0c0c0000;
+    // byte s of dwords 0..3 of v, as one dword
     auto pick = [&](const i32x4& v, int s) {
-      const int lo = __builtin_amdgcn_perm(v[1], v[0], s), hi = __builtin_amdgcn_perm(v[3], v[2], s);
+      const int sel = s | ((4 + s) << 8) | 0x0c0c0000;
+      const int lo = __builtin_amdgcn_perm(v[1], v[0], sel), hi = __builtin_amdgcn_perm(v[3], v[2], sel);
       return (int)__builtin_amdgcn_perm(hi, lo, 0x05040100);
     };
-    auto load_a = [&](int c) {
+    auto load_a = [&](auto FIRST, int c) {
       const int k0 = window(c);
+      const int kb = decltype(FIRST)::value ? min(16 * sc, code_pitch - 16) : (k0 >> 1) + 16 * sc;
+#pragma unroll
+      for (int i = 0; i < R; ++i) av[i] = *(const i32x4*)(row_ptr(i) + kb);
+      as = load_scales(FIRST, as_ptr, k0);
+    };
+    auto write_a = [&](int c) {
       // values before c * 512 were multiplied in the chunk before, values
       // past D do not exist: zero codes
-      const int k = k0 + 32 * sc;
+      const int k = window(c) + 32 * sc;
       const bool live = k >= c * kChunk && k < D;
-      const int kb = small ? min(16 * sc, code_pitch - 16) : (k0 >> 1) + 16 * sc;
+      const int b = c & 1;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        i32x4 v = *(const i32x4*)(arow[i] + kb);
+      for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) av[i][q] = live ? v[q] : 0;
-      }
-      if (tid < BM) as = load_scales(asrow, k0);
-    };
-    auto write_a = [&](int b) {
+        for (int q = 0; q < 4; ++q) av[i][q] = live ? av[i][q] : 0;
       write_rows(smem + b * stage_bytes, av);
-      if (tid < BM) {
-        i32x4 t;
+      i32x4 t;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) t[q] = pick(as, q | ((4 + q) << 8) | 0x0c0c0000);
-        *(i32x4*)(scl + (b * BM + tid) * 16) = t;
-      }
+      for (int q = 0; q < 4; ++q) t[q] = pick(as, q);
+      if (BM == kThreads || tid < BM) *(i32x4*)(scl + (b * BM + tid) * 16) = t;
     };
-    auto load_w = [&](auto B, int c) {
-      constexpr int b = decltype(B)::value;
-      const int k0 = window(c);
-      const char* wc = wbase + (k0 >> 1);
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          wq[b][cb][j] =
-              *(const i32x4*)(wc + woff[cb] + (small ? min(64 * j, code_pitch - 64) : 64 * j));
-        ws[b][cb] = load_scales(sbase + soff[cb], k0);
-      }
-    };
-    auto compute = [&](auto B) {
-      constexpr int b = decltype(B)::value;
+    auto chunk = [&](auto MORE, int c) {
+      constexpr bool more = decltype(MORE)::value;
+      const int b = c & 1;
       const char* st = smem + b * stage_bytes;
-      int sa[R], sw[CB];
+      int sw[CB], sa[R];
+#pragma unroll
+      for (int rb = 0; rb < RG; ++rb) fr[0][rb] = frag(st, rb, g);
 #pragma unroll
       for (int rb = 0; rb < R; ++rb)
         sa[rb] = *(const int*)(scl + (b * BM + 16 * rb + m) * 16 + 4 * g);
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) sw[cb] = pick(ws[b][cb], sel);
-#define MX_SLICE(J)                                                                              \
-  _Pragma("unroll") for (int rb = 0; rb < R; ++rb) {                                             \
-    const i32x4 f = frag(st, rb, 4 * J + g);                                                     \
-    const i32x8 fa = {f[0], f[1], f[2], f[3], 0, 0, 0, 0};                                       \
-    _Pragma("unroll") for (int cb = 0; cb < CB; ++cb) {                                          \
-      const i32x4 w = wq[b][cb][J];                                                              \
-      const i32x8 fw = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};                                     \
-      acc[rb][cb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                            \
-          fw, fa, acc[rb][cb], kFp4, kFp4, J, sw[cb], J, sa[rb]);                                \
-    }                                                                                            \
-  }
-      MX_SLICE(0)
-      MX_SLICE(1)
-      MX_SLICE(2)
-      MX_SLICE(3)
-#undef MX_SLICE
-    };
-    std::integral_constant<int, 0> P0;
-    std::integral_constant<int, 1> P1;
-    load_a(0);
-    load_w(P0, 0);
-    write_a(0);
-    lds_barrier();
-    auto step = [&](auto cur, auto nxt, int c) {
-      const bool more = c + 1 < KC;
-      if (more) {
-        load_a(c + 1);      // before the weights: the wait for it leaves them in flight
-        load_w(nxt, c + 1);
+      for (int cb = 0; cb < CB; ++cb) sw[cb] = pick(wn[cb], g);
+      if constexpr (more) {
+        load_a(No{}, c + 1);      // before the weights: the wait for it leaves them in flight
+        load_ws(No{}, c + 1);
       }
-      compute(cur);
-      if (more) write_a(decltype(nxt)::value);
+      each4([&](auto J) {
+        constexpr int j = decltype(J)::value;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const int n = j * NH + h;
+          if (opaque()) {
+            if (n + 1 < 4 * NH) {
+#pragma unroll
+              for (int rb = 0; rb < RG; ++rb)
+                fr[(n + 1) & 1][rb] =
+                    frag(st, ((n + 1) % NH) * RG + rb, 4 * ((n + 1) / NH) + g);
+            }
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+              const i32x4 f = fr[n & 1][r];
+              const i32x8 fa = {f[0], f[1], f[2], f[3], 0, 0, 0, 0};
+              const int rb = h * RG + r;
+#pragma unroll
+              for (int cb = 0; cb < CB; ++cb) {
+                const i32x4 w = wq[j][cb];
+                const i32x8 fw = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+                acc[rb][cb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    fw, fa, acc[rb][cb], kFp4, kFp4, j, sw[cb], j, sa[rb]);
+              }
+            }
+          }
+        }
+        if constexpr (more) load_w(No{}, J, c + 1);
+      });
+      if constexpr (more) write_a(c + 1);
       lds_barrier();
     };
-    for (int c = 0; c < KC; c += 2) {
-      step(P0, P1, c);
-      if (c + 1 < KC) step(P1, P0, c + 1);
-    }
+    load_a(Yes{}, 0);
+    write_a(0);
+    lds_barrier();
+    for (int c = 0; c + 1 < KC; ++c) chunk(Yes{}, c);
+    chunk(No{}, KC - 1);
   } else {
-    constexpr int PA = R <= 4 ? 4 : R <= 8 ? 2 : 1;   // row stages in flight in registers
+    constexpr int PA = R <= 4 ? 4 : 2;   // row stages in flight in registers
     i32x4 av[PA][R];
-    i32x4 wq[4][CB], ws[CB], wn[CB];
+    i32x4 ws[CB];
     const int S = 4 * KC;
     auto load_a = [&](i32x4* v, int s) {
-      const int k = window(s >> 2) + 128 * (s & 3);
-      const int kb = 2 * min(k, D - 128) + 16 * sc;
+      const int kb = 2 * min(window(s >> 2) + 128 * (s & 3), D - 128) + 16 * sc;
 #pragma unroll
-      for (int i = 0; i < R; ++i) v[i] = *(const i32x4*)(arow[i] + kb);
-    };
-    auto load_w = [&](auto J, int c) {
-      constexpr int j = decltype(J)::value;
-      const char* wc = wbase + (window(c) >> 1);
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-        wq[j][cb] =
-            *(const i32x4*)(wc + woff[cb] + (small ? min(64 * j, code_pitch - 64) : 64 * j));
+      for (int i = 0; i < R; ++i) v[i] = *(const i32x4*)(row_ptr(i) + kb);
     };
     auto compute = [&](auto J, int b) {
       constexpr int j = decltype(J)::value;
       const char* st = smem + b * stage_bytes;
-      bf16x8 fw[CB][4];
+      float sc2[CB];
+      bf16x8 fw[2][CB];
+      // e8m0 byte as an fp32 power of two (0xFF: NaN)
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        // e8m0 byte as an fp32 power of two (0xFF: NaN)
-        const float sc2 = __uint_as_float(__builtin_amdgcn_ubfe((unsigned)ws[cb][j], 8 * g, 8) << 23);
+      for (int cb = 0; cb < CB; ++cb)
+        sc2[cb] = __uint_as_float(__builtin_amdgcn_ubfe((unsigned)ws[cb][j], 8 * g, 8) << 23);
+      auto unpack = [&](bf16x8* o, int q) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int cb = 0; cb < CB; ++cb) {
           const unsigned u = (unsigned)wq[j][cb][q];
-          const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 0);
-          const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 1);
-          const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 2);
-          const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2, 3);
-          fw[cb][q] = bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+          const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 0);
+          const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 1);
+          const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 2);
+          const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 3);
+          o[cb] = bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
         }
-      }
+      };
+#pragma unroll
+      for (int rb = 0; rb < RG; ++rb) fr[0][rb] = frag(st, rb, 4 * g);
+      unpack(fw[0], 0);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int rb = 0; rb < R; ++rb) {
-          const bf16x8 fa = __builtin_bit_cast(bf16x8, frag(st, rb, 4 * g + q));
+        for (int h = 0; h < NH; ++h) {
+          const int n = q * NH + h;
+          if (opaque()) {
+            if (n + 1 < 4 * NH) {
 #pragma unroll
-          for (int cb = 0; cb < CB; ++cb)
-            acc[rb][cb] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[cb][q], fa, acc[rb][cb], 0, 0, 0);
+              for (int rb = 0; rb < RG; ++rb)
+                fr[(n + 1) & 1][rb] =
+                    frag(st, ((n + 1) % NH) * RG + rb, 4 * g + (n + 1) / NH);
+            }
+            if (h == NH - 1 && q < 3) unpack(fw[(q + 1) & 1], q + 1);
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+              const bf16x8 fa = __builtin_bit_cast(bf16x8, fr[n & 1][r]);
+              const int rb = h * RG + r;
+#pragma unroll
+              for (int cb = 0; cb < CB; ++cb)
+                acc[rb][cb] =
+                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[q & 1][cb], fa, acc[rb][cb], 0, 0, 0);
+            }
+          }
         }
     };
-    auto each4 = [&](auto&& f) {
-      f(std::integral_constant<int, 0>{});
-      f(std::integral_constant<int, 1>{});
-      f(std::integral_constant<int, 2>{});
-      f(std::integral_constant<int, 3>{});
-    };
-    // stage s's rows, then stages 1 .. PA in registers, chunk 0's weights
-    load_a(av[0], 0);
-    {
-      write_rows(smem, av[0]);
-    }
-#pragma unroll
-    for (int i = 1; i <= PA; ++i) load_a(av[i % PA], min(i, S - 1));
-#pragma unroll
-    for (int cb = 0; cb < CB; ++cb) ws[cb] = load_scales(sbase + soff[cb], 0);
-    each4([&](auto J) { load_w(J, 0); });
-    lds_barrier();
-    for (int c = 0; c < KC; ++c) {
-      const bool more = c + 1 < KC;
+    auto chunk = [&](auto MORE, int c) {
+      constexpr bool more = decltype(MORE)::value;
       const int k0 = window(c);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) ws[cb] = wn[cb];
       each4([&](auto J) {
         constexpr int j = decltype(J)::value;
         const int s = 4 * c + j;
-        if (s + 1 < S) {
+        if constexpr (more || j < 3) {
           i32x4* v = av[(j + 1) % PA];
           write_rows(smem + ((j + 1) & 1) * stage_bytes, v);
-          load_a(v, min(s + 1 + PA, S - 1));
+          if constexpr (more || j + 1 + PA < 4) load_a(v, min(s + 1 + PA, S - 1));
         }
+        if constexpr (more && j == 0) load_ws(No{}, c + 1);
+        // slices of the last chunk that an earlier one held, or past a short row
         const int k = k0 + 128 * j;
-        if (k >= c * kChunk && k < D) compute(J, j & 1);
-        if (more) {
-          if (j == 0) {
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
-              wn[cb] = load_scales(sbase + soff[cb], window(c + 1));
-          }
-          load_w(J, c + 1);
-        }
+        if (more || (k >= c * kChunk && k < D)) compute(J, j & 1);
+        if constexpr (more) load_w(No{}, J, c + 1);
         lds_barrier();
       });
+    };
+    // stage 0's rows, then stages 1 .. PA in registers
+    load_a(av[0], 0);
+    write_rows(smem, av[0]);
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) ws[cb] = wn[cb];
-    }
+    for (int i = 1; i <= PA; ++i) load_a(av[i % PA], min(i, S - 1));
+    lds_barrier();
+    for (int c = 0; c + 1 < KC; ++c) chunk(Yes{}, c);
+    chunk(No{}, KC - 1);
   }
 
   // ---- lane l: row 16 rb + l % 16, output columns col0 + 4 CBH g + [0, 4 CBH)
@@ -409,21 +456,23 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_small(GemmArgs p) {
   }
 }
 
-// m-tiles of up to 256 rows
+// m-tiles of up to kMaxRows rows
 template <bool A4, bool SW, typename OutT>
 __global__ __launch_bounds__(kThreads, 1) void gemm_large(GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<16, A4>()];
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<kMaxRows<A4> / 16, A4>()];
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
   if (t.z <= 64)
     tile<4, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
-  else if (t.z <= 128)
+  else if (!A4 || t.z <= 128)
     tile<8, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
-  else if (t.z <= 192)
-    tile<12, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
-  else
-    tile<16, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if constexpr (A4) {
+    if (t.z <= 192)
+      tile<12, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+    else
+      tile<16, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+  }
 }
 
 // cb: column blocks per wave of the small kernel (4, 2, and without SwiGLU 1)

@@ -12,17 +12,19 @@ constexpr int kListThreads = 1024;
 constexpr size_t kHeader = 256;
 
 inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
-inline size_t max_tiles(int rows_cap, int n_experts) {
-  return (size_t)rows_cap / kMaxRows + n_experts;
+// m-tiles of bm rows at most; workspaces hold the list of either form of rows
+inline int tile_rows(bool fp4_rows) { return fp4_rows ? kMaxRows<true> : kMaxRows<false>; }
+inline size_t max_tiles(int rows_cap, int n_experts, int bm) {
+  return (size_t)rows_cap / bm + n_experts;
 }
 
 // head: [0] m-tiles of more than 32 rows, [1] m-tiles of at most 32, [2] = 0
 // (where the first start), [3] = head[0] (where the others start).
-// An expert of m rows has m / 256 full m-tiles and a rest.  Rows are clamped
+// An expert of m rows has m / bm full m-tiles and a rest.  Rows are clamped
 // to [0, rows_cap) and the list to its capacity, so malformed offsets shrink
 // the work but never index past the buffers.
 __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restrict__ offsets,
-                                                         int n_experts, int rows_cap,
+                                                         int n_experts, int rows_cap, int bm,
                                                          int max_tiles, int* __restrict__ head,
                                                          int4* __restrict__ tiles) {
   __shared__ int2 wave_sum[kListThreads / kWave];
@@ -37,8 +39,8 @@ __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restri
   for (int e = lo; e < hi; ++e) {
     int r0, m;
     span(e, r0, m);
-    const int rest = m % kMaxRows;
-    mine.x += m / kMaxRows + (rest > kSmallRows ? 1 : 0);
+    const int rest = m % bm;
+    mine.x += m / bm + (rest > kSmallRows ? 1 : 0);
     mine.y += rest > 0 && rest <= kSmallRows ? 1 : 0;
   }
   int2 sum = mine;                       // inclusive over the wave's lanes
@@ -62,10 +64,10 @@ __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restri
   for (int e = lo; e < hi; ++e) {
     int r0, m;
     span(e, r0, m);
-    const int mt = (m + kMaxRows - 1) / kMaxRows;
+    const int mt = (m + bm - 1) / bm;
     for (int j = 0; j < mt; ++j) {
-      const int rows = min(kMaxRows, m - j * kMaxRows);
-      const int4 t = make_int4(e, r0 + j * kMaxRows, rows, mt);
+      const int rows = min(bm, m - j * bm);
+      const int4 t = make_int4(e, r0 + j * bm, rows, mt);
       if (rows > kSmallRows) {
         if (pl < nl) tiles[pl] = t;
         ++pl;
@@ -86,20 +88,21 @@ __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restri
 }  // namespace
 
 size_t tile_list_bytes(int rows_cap, int n_experts) {
-  return kHeader + align256(max_tiles(rows_cap, n_experts) * sizeof(int4));
+  return kHeader + align256(max_tiles(rows_cap, n_experts, kMaxRows<false>) * sizeof(int4));
 }
 
 bool grid_fits(int rows_cap, int n_experts, int N) {
-  const long long m = (long long)max_tiles(rows_cap, n_experts) + 8;
+  const long long m = (long long)max_tiles(rows_cap, n_experts, kMaxRows<false>) + 8;
   return m * (ceil_div((size_t)N, 64) + 1) < (1ll << 31) / kThreads;
 }
 
 hipError_t launch_tiles(const int32_t* offsets, int rows_cap, int n_experts, int rows_max,
-                        void* ws, hipStream_t s) {
+                        bool fp4_rows, void* ws, hipStream_t s) {
+  const int bm = tile_rows(fp4_rows);
   if (rows_max <= kSmallRows) return hipSuccess;   // one m-tile an expert, found by its number
   MOE_LAUNCH("mx_tiles", s,
-             mx_tiles<<<1, kListThreads, 0, s>>>(offsets, n_experts, rows_cap,
-                                                 (int)max_tiles(rows_cap, n_experts), (int*)ws,
+             mx_tiles<<<1, kListThreads, 0, s>>>(offsets, n_experts, rows_cap, bm,
+                                                 (int)max_tiles(rows_cap, n_experts, bm), (int*)ws,
                                                  (int4*)((char*)ws + kHeader)));
   return hipGetLastError();
 }
@@ -129,7 +132,7 @@ hipError_t launch_product(const void* a, const uint8_t* a_scales, const int32_t*
     p.tiles = (const int4*)((char*)ws + kHeader);
     p.count = head;
     p.first = head + 2;
-    const unsigned m = (unsigned)max_tiles(rows_cap, n_experts);
+    const unsigned m = (unsigned)max_tiles(rows_cap, n_experts, tile_rows(a_scales != nullptr));
     e = a_scales ? launch_gemm_large<true>(p, swiglu, out_dtype, m, s)
                  : launch_gemm_large<false>(p, swiglu, out_dtype, m, s);
     if (e != hipSuccess) return e;
