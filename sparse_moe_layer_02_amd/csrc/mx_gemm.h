@@ -47,7 +47,8 @@ constexpr int kChunk = 512;        // values of a weight row per load chunk
 // bound an expert of more than about 100 rows, and 256 rows' accumulators next
 // to the fragments in two forms do not fit the registers.
 template <bool A4> constexpr int kMaxRows = A4 ? 256 : 128;
-constexpr int kSmallRows = 32;     // m-tiles of the small-batch kernels
+constexpr int kSmallRows = 16;     // m-tiles of the small kernel
+constexpr int kMidRows = 64;       // ... and of the middle one
 using Yes = std::true_type;
 using No = std::false_type;
 constexpr int kFp4 = 4;            // the instruction's operand format code for e2m1
@@ -62,11 +63,10 @@ struct GemmArgs {
   const uint8_t* w;                // [E][N][D / 2]
   const uint8_t* w_scales;         // [E][N][D / 32]
   void* out;                       // [.][N] or, SwiGLU, [.][N / 2]
-  // list mode: tiles[first .. first + *count); direct mode (count NULL): the
-  // m-tile is expert number
+  // list mode: m-tiles tiles[span[0]] .. tiles[span[1] - 1]; direct mode (span
+  // NULL): m-tile number e is expert e's rows
   const int4* tiles;
-  const int* first;
-  const int* count;
+  const int* span;
   int NT;                          // column tiles
 };
 
@@ -427,9 +427,10 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& p, int4& t, int& nt) {
   const int b = blockIdx.x, slot = b >> 3;
   const int mt = (slot / p.NT) * 8 + (b & 7);
   nt = slot % p.NT;
-  if (p.count) {
-    if (mt >= *p.count) return false;
-    t = p.tiles[*p.first + mt];
+  if (p.span) {
+    const int at = p.span[0] + mt;
+    if (at >= p.span[1]) return false;
+    t = p.tiles[at];
     return true;
   }
   if (mt >= p.n_experts) return false;
@@ -439,99 +440,100 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& p, int4& t, int& nt) {
   return n > 0;
 }
 
-// m-tiles of at most 32 rows.  Direct mode is taken where no dispatch gives an
-// expert more; one that has more all the same is taken 32 rows at a time.
+// Three kernels by the m-tile's rows, since a kernel's registers are those of
+// its largest tile: with one of 32 rows beside it, that of 16 spilled.
+//
+// At most 16 rows.  Direct mode is taken where no dispatch gives an expert
+// more; one that has more all the same is taken 16 rows at a time.
 template <int CB, bool A4, bool SW, typename OutT>
 __global__ __launch_bounds__(kThreads, 2) void gemm_small(GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<2, A4>()];
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<1, A4>()];
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
-  for (int r = 0; r < t.z; r += kSmallRows) {
-    const int rows = min(kSmallRows, t.z - r);
-    if (rows <= 16)
-      tile<1, CB, A4, SW, OutT>(smem, p, t.x, t.y + r, rows, nt);
-    else
-      tile<2, CB, A4, SW, OutT>(smem, p, t.x, t.y + r, rows, nt);
-  }
+  int r = 0;
+  do {
+    // nothing of a turn is kept in registers for the next
+    asm volatile("" : "+s"(t.x), "+s"(nt));
+    tile<1, CB, A4, SW, OutT>(smem, p, t.x, t.y + r, min(kSmallRows, t.z - r), nt);
+    r += kSmallRows;
+  } while (r < t.z);
 }
 
-// m-tiles of up to kMaxRows rows
+// 17 to 64 rows.  bf16 rows: two column blocks a wave, so that the fragments
+// in both forms fit the registers of two blocks per CU.
+template <bool A4> constexpr int kMidCB = A4 ? 4 : 2;
+template <bool A4, bool SW, typename OutT>
+__global__ __launch_bounds__(kThreads, 2) void gemm_mid(GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<4, A4>()];
+  int4 t;
+  int nt;
+  if (!find_tile(p, t, nt)) return;
+  if (t.z <= 32)
+    tile<2, kMidCB<A4>, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else
+    tile<4, kMidCB<A4>, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+}
+
+// 65 to kMaxRows rows
 template <bool A4, bool SW, typename OutT>
 __global__ __launch_bounds__(kThreads, 1) void gemm_large(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) char smem[lds_bytes<kMaxRows<A4> / 16, A4>()];
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
-  if (t.z <= 64)
-    tile<4, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
-  else if (!A4 || t.z <= 128)
+  if constexpr (!A4) {
     tile<8, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
-  else if constexpr (A4) {
-    if (t.z <= 192)
+  } else {
+    if (t.z <= 128)
+      tile<8, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+    else if (t.z <= 192)
       tile<12, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
     else
       tile<16, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
   }
 }
 
-// cb: column blocks per wave of the small kernel (4, 2, and without SwiGLU 1)
+// Launches of one kind of rows.  kind 0: the small kernel, with cb column
+// blocks per wave (4, 2 and, without SwiGLU, 1); 1: the middle one; 2: the large.
 template <bool A4>
-hipError_t launch_gemm_small(GemmArgs p, bool swiglu, int out_dtype, int cb, unsigned mtiles,
-                             hipStream_t s);
-template <bool A4>
-hipError_t launch_gemm_large(GemmArgs p, bool swiglu, int out_dtype, unsigned mtiles,
-                             hipStream_t s);
+hipError_t launch_gemm(GemmArgs p, int kind, bool swiglu, int out_dtype, int cb, unsigned mtiles,
+                       hipStream_t s);
 
-template <bool A4>
-struct Launch {
-  template <int CB, bool SW, typename OutT>
-  static void small(GemmArgs& p, unsigned mtiles, hipStream_t s) {
-    const int width = SW ? p.N / 2 : p.N;
-    p.NT = (int)ceil_div(width, SW ? 32 * CB : 64 * CB);
-    const unsigned grid = ceil_div(mtiles, 8) * 8 * p.NT;
-    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
-               gemm_small<CB, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
-  }
-  template <bool SW, typename OutT>
-  static void small_cb(GemmArgs& p, int cb, unsigned mtiles, hipStream_t s) {
-    if (cb >= 4) return small<4, SW, OutT>(p, mtiles, s);
-    if constexpr (!SW) {
-      if (cb == 1) return small<1, SW, OutT>(p, mtiles, s);
-    }
-    return small<2, SW, OutT>(p, mtiles, s);
-  }
-  template <bool SW, typename OutT>
-  static void large(GemmArgs& p, unsigned mtiles, hipStream_t s) {
-    const int width = SW ? p.N / 2 : p.N;
-    p.NT = (int)ceil_div(width, SW ? 128 : 256);
-    const unsigned grid = ceil_div(mtiles, 8) * 8 * p.NT;
+template <bool A4, bool SW, typename OutT>
+void launch_gemm_t(GemmArgs& p, int kind, int cb, unsigned mtiles, hipStream_t s) {
+  const int width = SW ? p.N / 2 : p.N;
+  if (kind == 1) cb = kMidCB<A4>;
+  p.NT = (int)ceil_div(width, SW ? 32 * cb : 64 * cb);
+  const unsigned grid = ceil_div(mtiles, 8) * 8 * p.NT;
+  if (kind == 2) {
     MOE_LAUNCH(A4 ? "mx_gemm_large_fp4" : "mx_gemm_large_bf16", s,
                gemm_large<A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  } else if (kind == 1) {
+    MOE_LAUNCH(A4 ? "mx_gemm_mid_fp4" : "mx_gemm_mid_bf16", s,
+               gemm_mid<A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  } else if (cb == 4) {
+    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
+               gemm_small<4, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  } else if (cb == 2) {
+    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
+               gemm_small<2, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  } else if constexpr (!SW) {
+    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
+               gemm_small<1, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
   }
-};
+}
 
 #define MX_INSTANTIATE(A4)                                                                       \
   template <>                                                                                    \
-  hipError_t launch_gemm_small<A4>(GemmArgs p, bool swiglu, int out_dtype, int cb,               \
-                                   unsigned mtiles, hipStream_t s) {                             \
+  hipError_t launch_gemm<A4>(GemmArgs p, int kind, bool swiglu, int out_dtype, int cb,           \
+                             unsigned mtiles, hipStream_t s) {                                   \
     if (out_dtype == MOE_BF16)                                                                   \
-      swiglu ? Launch<A4>::small_cb<true, bf16>(p, cb, mtiles, s)                                \
-             : Launch<A4>::small_cb<false, bf16>(p, cb, mtiles, s);                              \
+      swiglu ? launch_gemm_t<A4, true, bf16>(p, kind, cb, mtiles, s)                             \
+             : launch_gemm_t<A4, false, bf16>(p, kind, cb, mtiles, s);                           \
     else                                                                                         \
-      swiglu ? Launch<A4>::small_cb<true, float>(p, cb, mtiles, s)                               \
-             : Launch<A4>::small_cb<false, float>(p, cb, mtiles, s);                             \
-    return hipGetLastError();                                                                    \
-  }                                                                                              \
-  template <>                                                                                    \
-  hipError_t launch_gemm_large<A4>(GemmArgs p, bool swiglu, int out_dtype, unsigned mtiles,      \
-                                   hipStream_t s) {                                              \
-    if (out_dtype == MOE_BF16)                                                                   \
-      swiglu ? Launch<A4>::large<true, bf16>(p, mtiles, s)                                       \
-             : Launch<A4>::large<false, bf16>(p, mtiles, s);                                     \
-    else                                                                                         \
-      swiglu ? Launch<A4>::large<true, float>(p, mtiles, s)                                      \
-             : Launch<A4>::large<false, float>(p, mtiles, s);                                    \
+      swiglu ? launch_gemm_t<A4, true, float>(p, kind, cb, mtiles, s)                            \
+             : launch_gemm_t<A4, false, float>(p, kind, cb, mtiles, s);                          \
     return hipGetLastError();                                                                    \
   }
 

@@ -18,16 +18,17 @@ inline size_t max_tiles(int rows_cap, int n_experts, int bm) {
   return (size_t)rows_cap / bm + n_experts;
 }
 
-// head: [0] m-tiles of more than 32 rows, [1] m-tiles of at most 32, [2] = 0
-// (where the first start), [3] = head[0] (where the others start).
-// An expert of m rows has m / bm full m-tiles and a rest.  Rows are clamped
-// to [0, rows_cap) and the list to its capacity, so malformed offsets shrink
-// the work but never index past the buffers.
+// The m-tiles of all experts, those of more than 64 rows first, then those of
+// 17 to 64, then the rest; head[0..3]: where each part starts and the last
+// ends.  An expert of m rows has m / bm full m-tiles and a rest.  Rows are
+// clamped to [0, rows_cap) and the list to its capacity, so malformed offsets
+// shrink the work but never index past the buffers.
 __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restrict__ offsets,
                                                          int n_experts, int rows_cap, int bm,
                                                          int max_tiles, int* __restrict__ head,
                                                          int4* __restrict__ tiles) {
-  __shared__ int2 wave_sum[kListThreads / kWave];
+  constexpr int kParts = 3;
+  __shared__ int wave_sum[kParts][kListThreads / kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int per = (n_experts + kListThreads - 1) / kListThreads;
   const int lo = min(n_experts, tid * per), hi = min(n_experts, lo + per);
@@ -35,53 +36,51 @@ __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restri
     r0 = min(max(offsets[e], 0), rows_cap);
     m = min(max(offsets[e + 1], r0), rows_cap) - r0;
   };
-  int2 mine = make_int2(0, 0);
+  auto part_of = [](int rows) { return rows > kMidRows ? 0 : rows > kSmallRows ? 1 : 2; };
+  int mine[kParts] = {0, 0, 0}, sum[kParts];
   for (int e = lo; e < hi; ++e) {
     int r0, m;
     span(e, r0, m);
-    const int rest = m % bm;
-    mine.x += m / bm + (rest > kSmallRows ? 1 : 0);
-    mine.y += rest > 0 && rest <= kSmallRows ? 1 : 0;
+    const int rest = m % bm, k = part_of(rest);
+    mine[0] += m / bm;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) mine[i] += rest > 0 && k == i ? 1 : 0;
   }
-  int2 sum = mine;                       // inclusive over the wave's lanes
-  for (int off = 1; off < kWave; off <<= 1) {
-    const int x = __shfl_up(sum.x, off), y = __shfl_up(sum.y, off);
-    if (lane >= off) {
-      sum.x += x;
-      sum.y += y;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    sum[i] = mine[i];                    // inclusive over the wave's lanes
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int v = __shfl_up(sum[i], off);
+      if (lane >= off) sum[i] += v;
     }
+    if (lane == kWave - 1) wave_sum[i][wave] = sum[i];
   }
-  if (lane == kWave - 1) wave_sum[wave] = sum;
   __syncthreads();
-  int2 before = make_int2(0, 0), all = make_int2(0, 0);
-  for (int w = 0; w < kListThreads / kWave; ++w) {
-    if (w == wave) before = all;
-    all.x += wave_sum[w].x;
-    all.y += wave_sum[w].y;
+  int at[kParts], end[kParts], start = 0;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    int before = 0, all = 0;
+    for (int w = 0; w < kListThreads / kWave; ++w) {
+      if (w == wave) before = all;
+      all += wave_sum[i][w];
+    }
+    at[i] = start + before + sum[i] - mine[i];
+    if (tid == 0) head[i] = start;
+    start = end[i] = min(start + all, max_tiles);
   }
-  const int nl = min(all.x, max_tiles), ns = min(all.y, max_tiles - nl);
-  int pl = before.x + sum.x - mine.x, ps = before.y + sum.y - mine.y;
+  if (tid == 0) head[kParts] = start;
   for (int e = lo; e < hi; ++e) {
     int r0, m;
     span(e, r0, m);
-    const int mt = (m + bm - 1) / bm;
-    for (int j = 0; j < mt; ++j) {
-      const int rows = min(bm, m - j * bm);
-      const int4 t = make_int4(e, r0 + j * bm, rows, mt);
-      if (rows > kSmallRows) {
-        if (pl < nl) tiles[pl] = t;
-        ++pl;
-      } else {
-        if (ps < ns) tiles[nl + ps] = t;
-        ++ps;
-      }
+    for (int j = 0; j < m; j += bm) {
+      const int rows = min(bm, m - j), k = part_of(rows);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+        if (k == i) {
+          if (at[i] < end[i]) tiles[at[i]] = make_int4(e, r0 + j, rows, 0);
+          ++at[i];
+        }
     }
-  }
-  if (tid == 0) {
-    head[0] = nl;
-    head[1] = ns;
-    head[2] = 0;
-    head[3] = nl;
   }
 }
 
@@ -125,26 +124,31 @@ hipError_t launch_product(const void* a, const uint8_t* a_scales, const int32_t*
   p.w = w;
   p.w_scales = w_scales;
   p.out = out;
-  int* head = (int*)ws;
-  const bool list = rows_max > kSmallRows;
+  const bool fp4 = a_scales != nullptr;
+  auto launch = [&](int kind, int cb, size_t mtiles) {
+    return fp4 ? launch_gemm<true>(p, kind, swiglu, out_dtype, cb, (unsigned)mtiles, s)
+               : launch_gemm<false>(p, kind, swiglu, out_dtype, cb, (unsigned)mtiles, s);
+  };
+  const size_t E = (size_t)n_experts, cap = (size_t)rows_cap;
   hipError_t e = hipSuccess;
-  if (list) {
+  if (rows_max > kSmallRows) {
+    const int* head = (const int*)ws;
     p.tiles = (const int4*)((char*)ws + kHeader);
-    p.count = head;
-    p.first = head + 2;
-    const unsigned m = (unsigned)max_tiles(rows_cap, n_experts, tile_rows(a_scales != nullptr));
-    e = a_scales ? launch_gemm_large<true>(p, swiglu, out_dtype, m, s)
-                 : launch_gemm_large<false>(p, swiglu, out_dtype, m, s);
+    // grids by what the rows allow at most: a part's m-tiles hold so many rows
+    // each, and an expert has one m-tile that is not full
+    if (rows_max > kMidRows) {
+      p.span = head;
+      e = launch(2, 4, std::min(cap / (kMidRows + 1), cap / tile_rows(fp4) + E));
+    }
+    p.span = head + 1;
+    if (e == hipSuccess) e = launch(1, 4, std::min(cap / (kSmallRows + 1), E));
     if (e != hipSuccess) return e;
-    p.count = head + 1;
-    p.first = head + 3;
+    p.span = head + 2;
   }
-  // at most one m-tile of at most 32 rows an expert
-  const unsigned hit = (unsigned)std::min(rows_cap, n_experts);
-  const unsigned blocks4 = hit * ceil_div(N, 256);
-  const int cb = blocks4 >= 512 ? 4 : 2 * blocks4 >= 512 ? 2 : 1;
-  return a_scales ? launch_gemm_small<true>(p, swiglu, out_dtype, cb, (unsigned)n_experts, s)
-                  : launch_gemm_small<false>(p, swiglu, out_dtype, cb, (unsigned)n_experts, s);
+  const size_t hit = std::min(cap, E);           // experts with rows, at most
+  const size_t blocks4 = hit * ceil_div(N, 256);
+  const int cb = blocks4 >= 512 ? 4 : 2 * blocks4 >= 512 || swiglu ? 2 : 1;
+  return launch(0, cb, p.span ? hit : E);
 }
 
 }  // namespace mx
