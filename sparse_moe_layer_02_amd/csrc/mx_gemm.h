@@ -46,11 +46,18 @@ constexpr int kChunk = 512;        // values of a weight row per load chunk
 // weights bound (its weights are loaded once).  bf16 rows: the matrix cores
 // bound an expert of more than about 100 rows, and 256 rows' accumulators next
 // to the fragments in two forms do not fit the registers.
-template <bool A4> constexpr int kMaxRows = A4 ? 256 : 128;
+template <bool A4> constexpr int kMaxRows = A4 ? 192 : 128;
 constexpr int kSmallRows = 16;     // m-tiles of the small kernel
 constexpr int kMidRows = 64;       // ... and of the middle one
 using Yes = std::true_type;
 using No = std::false_type;
+template <int I> using C = std::integral_constant<int, I>;
+template <class F> __device__ __forceinline__ void each4(F&& f) {
+  f(C<0>{});
+  f(C<1>{});
+  f(C<2>{});
+  f(C<3>{});
+}
 constexpr int kFp4 = 4;            // the instruction's operand format code for e2m1
 
 struct GemmArgs {
@@ -98,15 +105,18 @@ __device__ __forceinline__ void store_cols(OutT* o, const float* v) {
   }
 }
 
-// LDS of a tile of 16 R rows: two stages of rows, and for MXFP4 rows two
-// stages of their scales (one dword a row and 32-value group of a slice: byte
-// j is slice j's).
-template <int R, bool A4>
+// LDS of a tile of 16 R rows: two stages of rows; for MXFP4 rows two stages of
+// their scales (one dword a row and 32-value group of a slice: byte j is slice
+// j's); and for every wave 256 values of its 16 CB weight rows, with a chunk's
+// scales in the same form.
+template <int CB> constexpr int kWaveLds = 16 * CB * (128 + 16);
+template <int R, int CB, bool A4>
 constexpr int lds_bytes() {
-  return 2 * 16 * R * kPitch + (A4 ? 2 * 16 * R * 16 : 0);
+  return 2 * 16 * R * kPitch + (A4 ? 2 * 16 * R * 16 : 0) + 4 * kWaveLds<CB>;
 }
 
-template <int R, int CB, bool A4, bool SW, typename OutT>
+// NT: the weights are loaded past the caches (no other m-tile reads them)
+template <int R, int CB, bool A4, bool SW, bool NT, typename OutT>
 __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int row0, int rows,
                                      int nt) {
   static_assert(!SW || CB % 2 == 0, "gate and up blocks come in pairs");
@@ -122,51 +132,78 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   // first value of chunk c
   auto window = [&](int c) { return small ? 0 : min(c * kChunk, D - kChunk); };
 
-  auto each4 = [&](auto&& f) {
-    f(std::integral_constant<int, 0>{});
-    f(std::integral_constant<int, 1>{});
-    f(std::integral_constant<int, 2>{});
-    f(std::integral_constant<int, 3>{});
-  };
-
-  // ---- weights: lane l of block cb holds weight row (cb, l % 16), group g
+  // ---- weights.  Row r = 16 cb + i of the wave's 16 CB is row i of block cb.
   const int col0 = nt * (64 * CBH) + wave * (16 * CBH);   // first output column of the wave
   const char* wbase = (const char*)p.w + (size_t)e * N * code_pitch;
   const char* sbase = (const char*)p.w_scales + (size_t)e * N * scale_pitch;
-  uint32_t woff[CB], soff[CB];
+  auto weight_row = [&](int r) {
+    const int cb = r >> 4, i = r & 15, h = cb % CBH;
+    const int j = min(col0 + (i >> 2) * (4 * CBH) + 4 * h + (i & 3), width - 1);
+    return (uint32_t)(j + (SW && cb >= CBH ? width : 0));
+  };
+  // Codes come in steps of 256 values (half a chunk), 8 rows x 128 bytes a
+  // load: whole lines.  (Loads in the fragments' own layout, 16 rows x 64
+  // bytes with neighbouring lanes in different rows, take the address unit 58
+  // cycles each instead of 17: 4.2 TB/s.)  Two steps are in flight in
+  // registers; they pass through LDS, the wave's own part, where 16-byte
+  // pieces are XOR-swizzled by the row, to become fragments.
+  constexpr int NL = 2 * CB;                    // loads of a step
+  uint32_t woff[NL];
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb) {
-    const int h = cb % CBH;
-    const int j = min(col0 + (m >> 2) * (4 * CBH) + 4 * h + (m & 3), width - 1);
-    const uint32_t n = (uint32_t)(j + (SW && cb >= CBH ? width : 0));
-    woff[cb] = n * (uint32_t)code_pitch + 16u * g;
-    soff[cb] = n * (uint32_t)scale_pitch;
-  }
-  // Loads of chunk 0 also take rows shorter than a chunk (FIRST): the same
-  // places again instead of bytes past the row.  Loads inside the loop do not
-  // branch, so that the waits for them stay exact.
-  const int short_j = small ? scale_pitch / 4 - 1 : 3;    // last slice of a short row
+  for (int i = 0; i < NL; ++i)
+    woff[i] = weight_row(8 * i + (lane >> 3)) * (uint32_t)code_pitch;
+  const uint32_t soff = weight_row(lane & (16 * CB - 1)) * (uint32_t)scale_pitch;
+  // Loads in front of the loop also take rows shorter than a chunk (FIRST): the
+  // same places again instead of bytes past the row.  Loads inside the loop do
+  // not branch, so that the waits for them stay exact.
+  const int last_j = small ? scale_pitch / 4 - 1 : 3;     // last slice of a chunk
   auto load_scales = [&](auto FIRST, const char* s, int k0) -> i32x4 {
     if constexpr (!decltype(FIRST)::value) return *(const i32x4u*)(s + (k0 >> 5));
     i32x4 v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *(const int*)(s + 4 * min(j, short_j));
+    for (int j = 0; j < 4; ++j) v[j] = *(const int*)(s + 4 * min(j, last_j));
     return v;
   };
-  auto load_codes = [&](auto FIRST, const char* w, int j) {
-    return *(const i32x4*)(w + (decltype(FIRST)::value ? 64 * min(j, short_j) : 64 * j));
-  };
-
-  i32x4 wq[4][CB], wn[CB];                      // a chunk's codes; the next chunk's scales
-  auto load_w = [&](auto FIRST, auto J, int c) {
-    constexpr int j = decltype(J)::value;
-    const char* wc = wbase + (window(c) >> 1);
+  i32x4 wr[2][NL], wsr;                          // steps in flight; the next chunk's scales
+  auto load_w = [&](auto FIRST, auto B, int step) {
+    constexpr int b = decltype(B)::value;        // step & 1
+    const int at = 128 * b + 16 * (lane & 7);    // in the chunk
+    const char* wc = wbase + (window(step >> 1) >> 1) +
+                     (decltype(FIRST)::value ? min(at, 64 * last_j + 48) : at);
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) wq[j][cb] = load_codes(FIRST, wc + woff[cb], j);
+    for (int i = 0; i < NL; ++i) {
+      const i32x4* src = (const i32x4*)(wc + woff[i]);
+      wr[b][i] = NT ? __builtin_nontemporal_load(src) : *src;
+    }
   };
-  auto load_ws = [&](auto FIRST, int c) {
+  auto load_ws = [&](auto FIRST, int c) { wsr = load_scales(FIRST, sbase + soff, window(c)); };
+  char* wlds = smem + 2 * BM * kPitch + (A4 ? 2 * BM * 16 : 0) + wave * kWaveLds<CB>;
+  char* slds = wlds + 16 * CB * 128;
+  auto write_w = [&](auto B) {
+    constexpr int b = decltype(B)::value;
+    char* d = wlds + (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) wn[cb] = load_scales(FIRST, sbase + soff[cb], window(c));
+    for (int i = 0; i < NL; ++i) *(i32x4*)(d + i * 1024) = wr[b][i];
+  };
+  i32x4 fw[2][CB];                               // codes of a slice, by its parity
+  auto read_w = [&](auto T) {                    // slice T of the step in LDS
+    constexpr int t = decltype(T)::value;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+      fw[t][cb] = *(const i32x4*)(wlds + (16 * cb + m) * 128 + ((4 * t + g) ^ (m & 7)) * 16);
+  };
+  // byte s of dwords 0..3 of v, as one dword
+  auto pick = [&](const i32x4& v, int s) {
+    const int sel = s | ((4 + s) << 8) | 0x0c0c0000;
+    const int lo = __builtin_amdgcn_perm(v[1], v[0], sel), hi = __builtin_amdgcn_perm(v[3], v[2], sel);
+    return (int)__builtin_amdgcn_perm(hi, lo, 0x05040100);
+  };
+  auto scale_dwords = [&](const i32x4& v) { return i32x4{pick(v, 0), pick(v, 1), pick(v, 2), pick(v, 3)}; };
+  int sw[CB];                                    // byte j: the scale of slice j, group g
+  auto pass_scales = [&] {
+    if (16 * CB == 64 || lane < 16 * CB) *(i32x4*)(slds + lane * 16) = scale_dwords(wsr);
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) sw[cb] = *(const int*)(slds + (16 * cb + m) * 16 + 4 * g);
   };
 
   // ---- rows: thread t stages 16-byte chunk t % 16 of rows t / 16 + 16 i;
@@ -182,9 +219,10 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
 #pragma unroll
     for (int i = 0; i < NQ; ++i) src[i] = p.row_src[src[i]];
   }
-  // chunk 0's weights are on their way while the row indices arrive
+  // the first weights are on their way while the row indices arrive
   load_ws(Yes{}, 0);
-  each4([&](auto J) { load_w(Yes{}, J, 0); });
+  load_w(Yes{}, C<0>{}, 0);
+  load_w(Yes{}, C<1>{}, 1);
   if (p.row_src) {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) src[i] = min(max(src[i], 0) / p.K, p.T - 1);
@@ -211,12 +249,13 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     const int r = 16 * rb + m;
     return *(const i32x4*)(st + r * kPitch + swz16(r, chunk) * 16);
   };
-  // A chunk runs as groups of RG row blocks (RG * CB matrix instructions); the
-  // fragments of a group are read from LDS before the group in front of it is
-  // multiplied.  Each group is a basic block of its own, behind a branch on a
-  // value the compiler cannot see through: matrix instructions have no side
-  // effects, and without the branches they are all moved behind the waits for
-  // the next chunk's loads, which then hide behind nothing.
+  // Multiplications run in groups of RG row blocks (RG * CB matrix
+  // instructions); a group's row fragments are read from LDS before the group
+  // in front of it is multiplied, a slice's weight fragments a slice before.
+  // Each group is a basic block of its own, behind a branch on a value the
+  // compiler cannot see through: matrix instructions have no side effects, and
+  // without the branches they are all moved behind the waits for the next
+  // chunk's loads, which then hide behind nothing.
   constexpr int RG = R < 4 ? R : 4;
   constexpr int NH = R / RG;                     // groups per slice
   static_assert(R % RG == 0, "whole groups");
@@ -226,23 +265,45 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     asm volatile("" : "+s"(one));
     return one != 0;
   };
+  // The weights' part of slice J of chunk c, before its multiplications: the
+  // next slice's fragments, and at the end of a step the next step's codes
+  // into LDS and the loads of the step two further on.  AHEAD: chunks that
+  // follow c, as far as 2.
+  auto advance_w = [&](auto AHEAD, auto J, int c) {
+    constexpr int ahead = decltype(AHEAD)::value, j = decltype(J)::value;
+    if constexpr (j % 2 == 0) {
+      read_w(C<1>{});
+    } else if constexpr (j == 1 || ahead > 0) {
+      write_w(C<(j + 1) / 2 % 2>{});
+      // j = 1: step 2c + 3 of the next chunk; j = 3: step 2c + 4 of the one after
+      if constexpr (ahead > j / 2) load_w(No{}, C<(j + 1) / 2 % 2>{}, 2 * c + (j + 5) / 2);
+      read_w(C<0>{});
+    }
+  };
+  // Chunks in order, told how many follow.
+  auto sweep = [&](auto&& chunk) {
+    for (int c = 0; c + 2 < KC; ++c) chunk(C<2>{}, c);
+    if (KC >= 2) chunk(C<1>{}, KC - 2);
+    chunk(C<0>{}, KC - 1);
+  };
+  // In front of the sweep: step 0 in LDS, its first fragments, step 2 on its way.
+  auto first_w = [&] {
+    write_w(C<0>{});
+    if (KC >= 2) load_w(No{}, C<0>{}, 2);
+    pass_scales();
+    read_w(C<0>{});
+  };
 
   if constexpr (A4) {
     char* scl = smem + 2 * stage_bytes;
     const char* as_ptr = (const char*)p.a_scales + (size_t)src[R] * scale_pitch;
     i32x4 av[R], as;
-    // byte s of dwords 0..3 of v, as one dword
-    auto pick = [&](const i32x4& v, int s) {
-      const int sel = s | ((4 + s) << 8) | 0x0c0c0000;
-      const int lo = __builtin_amdgcn_perm(v[1], v[0], sel), hi = __builtin_amdgcn_perm(v[3], v[2], sel);
-      return (int)__builtin_amdgcn_perm(hi, lo, 0x05040100);
-    };
     auto load_a = [&](auto FIRST, int c) {
-      const int k0 = window(c);
-      const int kb = decltype(FIRST)::value ? min(16 * sc, code_pitch - 16) : (k0 >> 1) + 16 * sc;
+      const int kb = (window(c) >> 1) +
+                     (decltype(FIRST)::value ? min(16 * sc, 64 * last_j + 48) : 16 * sc);
 #pragma unroll
       for (int i = 0; i < R; ++i) av[i] = *(const i32x4*)(row_ptr(i) + kb);
-      as = load_scales(FIRST, as_ptr, k0);
+      as = load_scales(FIRST, as_ptr, window(c));
     };
     auto write_a = [&](int c) {
       // values before c * 512 were multiplied in the chunk before, values
@@ -255,29 +316,26 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
 #pragma unroll
         for (int q = 0; q < 4; ++q) av[i][q] = live ? av[i][q] : 0;
       write_rows(smem + b * stage_bytes, av);
-      i32x4 t;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) t[q] = pick(as, q);
+      const i32x4 t = scale_dwords(as);
       if (BM == kThreads || tid < BM) *(i32x4*)(scl + (b * BM + tid) * 16) = t;
     };
-    auto chunk = [&](auto MORE, int c) {
-      constexpr bool more = decltype(MORE)::value;
+    auto chunk = [&](auto AHEAD, int c) {
+      constexpr bool more = decltype(AHEAD)::value > 0;
       const int b = c & 1;
       const char* st = smem + b * stage_bytes;
-      int sw[CB], sa[R];
+      int sa[R];
 #pragma unroll
       for (int rb = 0; rb < RG; ++rb) fr[0][rb] = frag(st, rb, g);
 #pragma unroll
       for (int rb = 0; rb < R; ++rb)
         sa[rb] = *(const int*)(scl + (b * BM + 16 * rb + m) * 16 + 4 * g);
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) sw[cb] = pick(wn[cb], g);
       if constexpr (more) {
-        load_a(No{}, c + 1);      // before the weights: the wait for it leaves them in flight
-        load_ws(No{}, c + 1);
+        load_ws(No{}, c + 1);     // before the codes: the waits for these leave them in flight
+        load_a(No{}, c + 1);
       }
       each4([&](auto J) {
         constexpr int j = decltype(J)::value;
+        advance_w(AHEAD, J, c);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const int n = j * NH + h;
@@ -295,47 +353,48 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
               const int rb = h * RG + r;
 #pragma unroll
               for (int cb = 0; cb < CB; ++cb) {
-                const i32x4 w = wq[j][cb];
-                const i32x8 fw = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+                const i32x4 w = fw[j & 1][cb];
+                const i32x8 fb = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
                 acc[rb][cb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    fw, fa, acc[rb][cb], kFp4, kFp4, j, sw[cb], j, sa[rb]);
+                    fb, fa, acc[rb][cb], kFp4, kFp4, j, sw[cb], j, sa[rb]);
               }
             }
           }
         }
-        if constexpr (more) load_w(No{}, J, c + 1);
       });
-      if constexpr (more) write_a(c + 1);
+      if constexpr (more) {
+        write_a(c + 1);
+        pass_scales();
+      }
       lds_barrier();
     };
     load_a(Yes{}, 0);
+    first_w();
     write_a(0);
     lds_barrier();
-    for (int c = 0; c + 1 < KC; ++c) chunk(Yes{}, c);
-    chunk(No{}, KC - 1);
+    sweep(chunk);
   } else {
-    constexpr int PA = R <= 4 ? 4 : 2;   // row stages in flight in registers
+    constexpr int PA = R <= 2 ? 4 : 2;   // row stages in flight in registers
     i32x4 av[PA][R];
-    i32x4 ws[CB];
     const int S = 4 * KC;
     auto load_a = [&](i32x4* v, int s) {
       const int kb = 2 * min(window(s >> 2) + 128 * (s & 3), D - 128) + 16 * sc;
 #pragma unroll
       for (int i = 0; i < R; ++i) v[i] = *(const i32x4*)(row_ptr(i) + kb);
     };
-    auto compute = [&](auto J, int b) {
+    auto compute = [&](auto J) {
       constexpr int j = decltype(J)::value;
-      const char* st = smem + b * stage_bytes;
+      const char* st = smem + (j & 1) * stage_bytes;
       float sc2[CB];
-      bf16x8 fw[2][CB];
+      bf16x8 fb[2][CB];
       // e8m0 byte as an fp32 power of two (0xFF: NaN)
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb)
-        sc2[cb] = __uint_as_float(__builtin_amdgcn_ubfe((unsigned)ws[cb][j], 8 * g, 8) << 23);
+        sc2[cb] = __uint_as_float(__builtin_amdgcn_ubfe((unsigned)sw[cb], 8 * j, 8) << 23);
       auto unpack = [&](bf16x8* o, int q) {
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-          const unsigned u = (unsigned)wq[j][cb][q];
+          const unsigned u = (unsigned)fw[j & 1][cb][q];
           const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 0);
           const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 1);
           const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 2);
@@ -345,7 +404,7 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
       };
 #pragma unroll
       for (int rb = 0; rb < RG; ++rb) fr[0][rb] = frag(st, rb, 4 * g);
-      unpack(fw[0], 0);
+      unpack(fb[0], 0);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -358,7 +417,7 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
                 fr[(n + 1) & 1][rb] =
                     frag(st, ((n + 1) % NH) * RG + rb, 4 * g + (n + 1) / NH);
             }
-            if (h == NH - 1 && q < 3) unpack(fw[(q + 1) & 1], q + 1);
+            if (h == NH - 1 && q < 3) unpack(fb[(q + 1) & 1], q + 1);
 #pragma unroll
             for (int r = 0; r < RG; ++r) {
               const bf16x8 fa = __builtin_bit_cast(bf16x8, fr[n & 1][r]);
@@ -366,16 +425,15 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
 #pragma unroll
               for (int cb = 0; cb < CB; ++cb)
                 acc[rb][cb] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[q & 1][cb], fa, acc[rb][cb], 0, 0, 0);
+                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q & 1][cb], fa, acc[rb][cb], 0, 0, 0);
             }
           }
         }
     };
-    auto chunk = [&](auto MORE, int c) {
-      constexpr bool more = decltype(MORE)::value;
+    auto chunk = [&](auto AHEAD, int c) {
+      constexpr bool more = decltype(AHEAD)::value > 0;
       const int k0 = window(c);
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) ws[cb] = wn[cb];
+      if constexpr (more) load_ws(No{}, c + 1);
       each4([&](auto J) {
         constexpr int j = decltype(J)::value;
         const int s = 4 * c + j;
@@ -384,22 +442,22 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
           write_rows(smem + ((j + 1) & 1) * stage_bytes, v);
           if constexpr (more || j + 1 + PA < 4) load_a(v, min(s + 1 + PA, S - 1));
         }
-        if constexpr (more && j == 0) load_ws(No{}, c + 1);
-        // slices of the last chunk that an earlier one held, or past a short row
+        advance_w(AHEAD, J, c);
+        // not the slices that the chunk before holds, nor those past a short row
         const int k = k0 + 128 * j;
-        if (more || (k >= c * kChunk && k < D)) compute(J, j & 1);
-        if constexpr (more) load_w(No{}, J, c + 1);
+        if (k >= c * kChunk && k < D) compute(J);
+        if constexpr (more && j == 3) pass_scales();
         lds_barrier();
       });
     };
     // stage 0's rows, then stages 1 .. PA in registers
     load_a(av[0], 0);
+    first_w();
     write_rows(smem, av[0]);
 #pragma unroll
     for (int i = 1; i <= PA; ++i) load_a(av[i % PA], min(i, S - 1));
     lds_barrier();
-    for (int c = 0; c + 1 < KC; ++c) chunk(Yes{}, c);
-    chunk(No{}, KC - 1);
+    sweep(chunk);
   }
 
   // ---- lane l: row 16 rb + l % 16, output columns col0 + 4 CBH g + [0, 4 CBH)
@@ -447,50 +505,49 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& p, int4& t, int& nt) {
 // more; one that has more all the same is taken 16 rows at a time.
 template <int CB, bool A4, bool SW, typename OutT>
 __global__ __launch_bounds__(kThreads, 2) void gemm_small(GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<1, A4>()];
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<1, CB, A4>()];
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
   int r = 0;
   do {
     // nothing of a turn is kept in registers for the next
-    asm volatile("" : "+s"(t.x), "+s"(nt));
-    tile<1, CB, A4, SW, OutT>(smem, p, t.x, t.y + r, min(kSmallRows, t.z - r), nt);
+    int e = __builtin_amdgcn_readfirstlane(t.x), n = __builtin_amdgcn_readfirstlane(nt);
+    asm volatile("" : "+s"(e), "+s"(n));
+    tile<1, CB, A4, SW, true, OutT>(smem, p, e, t.y + r, min(kSmallRows, t.z - r), n);
     r += kSmallRows;
   } while (r < t.z);
 }
 
-// 17 to 64 rows.  bf16 rows: two column blocks a wave, so that the fragments
+// 17 to 64 rows, two column blocks a wave, so that the fragments
 // in both forms fit the registers of two blocks per CU.
-template <bool A4> constexpr int kMidCB = A4 ? 4 : 2;
+constexpr int kMidCB = 2;
 template <bool A4, bool SW, typename OutT>
 __global__ __launch_bounds__(kThreads, 2) void gemm_mid(GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<4, A4>()];
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<4, kMidCB, A4>()];
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
   if (t.z <= 32)
-    tile<2, kMidCB<A4>, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+    tile<2, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
   else
-    tile<4, kMidCB<A4>, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+    tile<4, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
 }
 
 // 65 to kMaxRows rows
 template <bool A4, bool SW, typename OutT>
 __global__ __launch_bounds__(kThreads, 1) void gemm_large(GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<kMaxRows<A4> / 16, A4>()];
+  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<kMaxRows<A4> / 16, 4, A4>()];
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
   if constexpr (!A4) {
-    tile<8, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+    tile<8, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
   } else {
     if (t.z <= 128)
-      tile<8, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
-    else if (t.z <= 192)
-      tile<12, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+      tile<8, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
     else
-      tile<16, 4, A4, SW, OutT>(smem, p, t.x, t.y, t.z, nt);
+      tile<12, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
   }
 }
 
@@ -503,7 +560,7 @@ hipError_t launch_gemm(GemmArgs p, int kind, bool swiglu, int out_dtype, int cb,
 template <bool A4, bool SW, typename OutT>
 void launch_gemm_t(GemmArgs& p, int kind, int cb, unsigned mtiles, hipStream_t s) {
   const int width = SW ? p.N / 2 : p.N;
-  if (kind == 1) cb = kMidCB<A4>;
+  if (kind == 1) cb = kMidCB;
   p.NT = (int)ceil_div(width, SW ? 32 * cb : 64 * cb);
   const unsigned grid = ceil_div(mtiles, 8) * 8 * p.NT;
   if (kind == 2) {
