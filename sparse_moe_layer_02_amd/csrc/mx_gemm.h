@@ -36,6 +36,7 @@ namespace mx {
 
 typedef __attribute__((__vector_size__(8 * sizeof(int)))) int i32x8;
 typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
 // a 16-byte load at a 4-byte aligned address (scale rows)
 typedef i32x4 __attribute__((aligned(4))) i32x4u;
 
@@ -52,12 +53,13 @@ constexpr int kMidRows = 64;       // ... and of the middle one
 using Yes = std::true_type;
 using No = std::false_type;
 template <int I> using C = std::integral_constant<int, I>;
-template <class F> __device__ __forceinline__ void each4(F&& f) {
-  f(C<0>{});
-  f(C<1>{});
-  f(C<2>{});
-  f(C<3>{});
+template <int N, int I = 0, class F> __device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(C<I>{});
+    each<N, I + 1>(f);
+  }
 }
+template <class F> __device__ __forceinline__ void each4(F&& f) { each<4>(f); }
 constexpr int kFp4 = 4;            // the instruction's operand format code for e2m1
 
 struct GemmArgs {
@@ -77,7 +79,7 @@ struct GemmArgs {
   int NT;                          // column tiles
 };
 
-__device__ __forceinline__ int swz16(int row, int chunk) { return chunk ^ (row & 15); }
+__device__ __forceinline__ int swz16(int row, int at) { return at ^ (row & 15); }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
@@ -110,20 +112,54 @@ __device__ __forceinline__ void store_cols(OutT* o, const float* v) {
 // j's); and for every wave 256 values of its 16 CB weight rows, with a chunk's
 // scales in the same form.
 template <int CB> constexpr int kWaveLds = 16 * CB * (128 + 16);
+// (R: rows / 16)
 template <int R, int CB, bool A4>
 constexpr int lds_bytes() {
   return 2 * 16 * R * kPitch + (A4 ? 2 * 16 * R * 16 : 0) + 4 * kWaveLds<CB>;
 }
 
-// NT: the weights are loaded past the caches (no other m-tile reads them)
-template <int R, int CB, bool A4, bool SW, bool NT, typename OutT>
+// One block of matrix instructions of MS x MS outputs: 16 or 32.  Lane l holds
+// row l % MS of either operand and one 32-value block of it, number l / MS of
+// the instruction's 4 (MS = 16) or 2; a slice of 128 values is kU instructions.
+template <int MS> struct Mma;
+template <> struct Mma<16> {
+  typedef f32x4 Acc;
+  static constexpr int kU = 1;
+  static __device__ __forceinline__ Acc bf16_(bf16x8 w, bf16x8 a, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, a, c, 0, 0, 0);
+  }
+  template <int B>
+  static __device__ __forceinline__ Acc fp4(i32x8 w, i32x8 a, Acc c, int sw, int sa) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, kFp4, kFp4, B, sw, B, sa);
+  }
+};
+template <> struct Mma<32> {
+  typedef f32x16 Acc;
+  static constexpr int kU = 2;
+  static __device__ __forceinline__ Acc bf16_(bf16x8 w, bf16x8 a, Acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, a, c, 0, 0, 0);
+  }
+  template <int B>
+  static __device__ __forceinline__ Acc fp4(i32x8 w, i32x8 a, Acc c, int sw, int sa) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, kFp4, kFp4, B, sw, B, sa);
+  }
+};
+
+// One tile: RB blocks of MS rows times 4 waves of 16 CB weight rows.
+// NT: the weights are loaded past the caches (no other m-tile reads them).
+template <int MS, int RB, int CB, bool A4, bool SW, bool NT, typename OutT>
 __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int row0, int rows,
                                      int nt) {
-  static_assert(!SW || CB % 2 == 0, "gate and up blocks come in pairs");
-  constexpr int CBH = SW ? CB / 2 : CB;         // blocks of output columns
-  constexpr int BM = 16 * R;
+  using M = Mma<MS>;
+  constexpr int BM = MS * RB;                   // rows
+  constexpr int NB = 16 * CB / MS;              // weight blocks of a wave
+  constexpr int U = M::kU, G = 64 / MS;         // instructions of a slice; 32-value blocks of one
+  constexpr int SL = 16 * CB / G;               // outputs of a lane per row
+  constexpr int kAcc = MS * MS / 64;
+  constexpr int WC = SW ? 8 * CB : 16 * CB;     // output columns of a wave
+  static_assert(NB >= 1 && (!SW || SL % 8 == 0), "gate and up in one lane, 4 at a time");
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int m = lane & 15, g = lane >> 4;
+  const int m = lane & (MS - 1), g = lane / MS;
   const int D = p.D, N = p.N;
   const int width = SW ? N / 2 : N;             // output columns
   const int code_pitch = D >> 1, scale_pitch = D >> 5;
@@ -132,14 +168,21 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   // first value of chunk c
   auto window = [&](int c) { return small ? 0 : min(c * kChunk, D - kChunk); };
 
-  // ---- weights.  Row r = 16 cb + i of the wave's 16 CB is row i of block cb.
-  const int col0 = nt * (64 * CBH) + wave * (16 * CBH);   // first output column of the wave
+  // ---- weights.  Row r = MS b + i of the wave's 16 CB is row i of block b.  An
+  // instruction leaves a lane rows 4 g + (0..3) of its 16, or rows 8 q + 4 g +
+  // (0..3) of its 32; which weight row each is makes the lane's SL outputs
+  // consecutive columns, with SwiGLU its first half the gates and its second
+  // the ups of the same columns.
+  const int col0 = nt * (4 * WC) + wave * WC;   // first output column of the wave
   const char* wbase = (const char*)p.w + (size_t)e * N * code_pitch;
   const char* sbase = (const char*)p.w_scales + (size_t)e * N * scale_pitch;
   auto weight_row = [&](int r) {
-    const int cb = r >> 4, i = r & 15, h = cb % CBH;
-    const int j = min(col0 + (i >> 2) * (4 * CBH) + 4 * h + (i & 3), width - 1);
-    return (uint32_t)(j + (SW && cb >= CBH ? width : 0));
+    const int b = r / MS, i = r % MS;
+    const int gi = MS == 16 ? i >> 2 : (i >> 2) & 1;
+    const int slot = MS == 16 ? 4 * b + (i & 3) : 16 * b + 4 * (i >> 3) + (i & 3);
+    constexpr int per = SW ? SL / 2 : SL;
+    const int j = min(col0 + gi * per + slot % per, width - 1);
+    return (uint32_t)(j + (slot >= per ? width : 0));
   };
   // Codes come in steps of 256 values (half a chunk), 8 rows x 128 bytes a
   // load: whole lines.  (Loads in the fragments' own layout, 16 rows x 64
@@ -185,29 +228,54 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
 #pragma unroll
     for (int i = 0; i < NL; ++i) *(i32x4*)(d + i * 1024) = wr[b][i];
   };
-  i32x4 fw[2][CB];                               // codes of a slice, by its parity
+  i32x4 fw[2][NB][U];                            // codes of a slice, by its parity
   auto read_w = [&](auto T) {                    // slice T of the step in LDS
     constexpr int t = decltype(T)::value;
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
-      fw[t][cb] = *(const i32x4*)(wlds + (16 * cb + m) * 128 + ((4 * t + g) ^ (m & 7)) * 16);
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        fw[t][b][u] = *(const i32x4*)(wlds + (MS * b + m) * 128 +
+                                      ((4 * t + G * u + g) ^ (m & 7)) * 16);
   };
-  // byte s of dwords 0..3 of v, as one dword
-  auto pick = [&](const i32x4& v, int s) {
-    const int sel = s | ((4 + s) << 8) | 0x0c0c0000;
-    const int lo = __builtin_amdgcn_perm(v[1], v[0], sel), hi = __builtin_amdgcn_perm(v[3], v[2], sel);
-    return (int)__builtin_amdgcn_perm(hi, lo, 0x05040100);
+  // A row's 16 scales of a chunk (dword j: slice j) as the lanes use them: MS =
+  // 16: dword g holds group g of the 4 slices; MS = 32: dwords 2 g + w hold
+  // groups g and 2 + g of slices 2 w and 2 w + 1.
+  auto scale_dwords = [&](const i32x4& v) {
+    if constexpr (MS == 16) {
+      i32x4 t;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int sel = s | ((4 + s) << 8) | 0x0c0c0000;
+        t[s] = (int)__builtin_amdgcn_perm(__builtin_amdgcn_perm(v[3], v[2], sel),
+                                          __builtin_amdgcn_perm(v[1], v[0], sel), 0x05040100);
+      }
+      return t;
+    } else {
+      return i32x4{(int)__builtin_amdgcn_perm(v[1], v[0], 0x06040200),
+                   (int)__builtin_amdgcn_perm(v[3], v[2], 0x06040200),
+                   (int)__builtin_amdgcn_perm(v[1], v[0], 0x07050301),
+                   (int)__builtin_amdgcn_perm(v[3], v[2], 0x07050301)};
+    }
   };
-  auto scale_dwords = [&](const i32x4& v) { return i32x4{pick(v, 0), pick(v, 1), pick(v, 2), pick(v, 3)}; };
-  int sw[CB];                                    // byte j: the scale of slice j, group g
+  // byte kByte(j, u) of dword kDword(j): the scale of a lane's block in
+  // instruction u of slice j
+  constexpr auto kByte = [](int j, int u) { return MS == 16 ? j : 2 * (j & 1) + u; };
+  constexpr auto kDword = [](int j) { return MS == 16 ? 0 : j >> 1; };
+  auto read_scales = [&](const char* s, int* d) {
+#pragma unroll
+    for (int w = 0; w < U; ++w) d[w] = *(const int*)(s + (U * g + w) * 4);
+  };
+  int sw[NB][U];
   auto pass_scales = [&] {
     if (16 * CB == 64 || lane < 16 * CB) *(i32x4*)(slds + lane * 16) = scale_dwords(wsr);
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) sw[cb] = *(const int*)(slds + (16 * cb + m) * 16 + 4 * g);
+    for (int b = 0; b < NB; ++b) read_scales(slds + (MS * b + m) * 16, sw[b]);
   };
 
   // ---- rows: thread t stages 16-byte chunk t % 16 of rows t / 16 + 16 i;
   // rows past the tile's are its last one again (never stored)
+  constexpr int R = BM / 16;
   const int sr = tid >> 4, sc = tid & 15;
   const int a_pitch = A4 ? code_pitch : 2 * D;
   constexpr int NQ = A4 ? R + 1 : R;
@@ -232,43 +300,50 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   for (int i = 0; i < R; ++i) arow[i] = (uint32_t)(((size_t)src[i] * a_pitch) >> 4);
   auto row_ptr = [&](int i) { return (const char*)p.a + ((size_t)arow[i] << 4); };
 
-  f32x4 acc[R][CB];
+  typename M::Acc acc[RB][NB];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int i = 0; i < RB; ++i)
 #pragma unroll
-    for (int j = 0; j < CB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int k = 0; k < kAcc; ++k) acc[i][j][k] = 0.0f;
   constexpr int stage_bytes = BM * kPitch;
+  // A lane's pieces of a row: MXFP4 4 j + b for block b of slice j; bf16 4 b + q
+  // for fragment q of block b, kept at place 4 q + b, so that the lanes of
+  // either read, which are served in an order that mixes rows of neighbouring
+  // groups, meet different banks.
+  const int place = A4 ? sc : 4 * (sc & 3) + (sc >> 2);
   auto write_rows = [&](char* st, const i32x4* v) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int r = sr + 16 * i;
-      *(i32x4*)(st + r * kPitch + swz16(r, sc) * 16) = v[i];
+      *(i32x4*)(st + r * kPitch + swz16(r, place) * 16) = v[i];
     }
   };
-  auto frag = [&](const char* st, int rb, int chunk) {
-    const int r = 16 * rb + m;
-    return *(const i32x4*)(st + r * kPitch + swz16(r, chunk) * 16);
+  auto frag = [&](const char* st, int rb, int at) {
+    const int r = MS * rb + m;
+    return *(const i32x4*)(st + r * kPitch + swz16(r, at) * 16);
   };
-  // Multiplications run in groups of RG row blocks (RG * CB matrix
+  // Multiplications run in groups of RG row blocks (RG * NB matrix
   // instructions); a group's row fragments are read from LDS before the group
   // in front of it is multiplied, a slice's weight fragments a slice before.
   // Each group is a basic block of its own, behind a branch on a value the
   // compiler cannot see through: matrix instructions have no side effects, and
   // without the branches they are all moved behind the waits for the next
   // chunk's loads, which then hide behind nothing.
-  constexpr int RG = R < 4 ? R : 4;
-  constexpr int NH = R / RG;                     // groups per slice
-  static_assert(R % RG == 0, "whole groups");
+  constexpr int RG = RB <= 5 ? RB : RB / 2;
+  constexpr int NH = RB / RG;                    // groups per instruction step
+  static_assert(RB % RG == 0, "whole groups");
   i32x4 fr[2][RG];
-  auto opaque = [&] {
-    int one = 1;
-    asm volatile("" : "+s"(one));
-    return one != 0;
+  auto opaque = [&](int v) {
+    v = __builtin_amdgcn_readfirstlane(v);
+    asm volatile("" : "+s"(v));
+    return v != 0;
   };
-  // The weights' part of slice J of chunk c, before its multiplications: the
-  // next slice's fragments, and at the end of a step the next step's codes
-  // into LDS and the loads of the step two further on.  AHEAD: chunks that
-  // follow c, as far as 2.
+  // The weights' part of slice J of chunk c, between its groups: the next
+  // slice's fragments, and at the end of a step the next step's codes into LDS
+  // and the loads of the step two further on.  AHEAD: chunks that follow c, as
+  // far as 2.
   auto advance_w = [&](auto AHEAD, auto J, int c) {
     constexpr int ahead = decltype(AHEAD)::value, j = decltype(J)::value;
     if constexpr (j % 2 == 0) {
@@ -295,6 +370,7 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   };
 
   if constexpr (A4) {
+    constexpr int NG = U * NH;                   // groups per slice
     char* scl = smem + 2 * stage_bytes;
     const char* as_ptr = (const char*)p.a_scales + (size_t)src[R] * scale_pitch;
     i32x4 av[R], as;
@@ -323,47 +399,51 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
       constexpr bool more = decltype(AHEAD)::value > 0;
       const int b = c & 1;
       const char* st = smem + b * stage_bytes;
-      int sa[R];
+      int sa[RB][U];
 #pragma unroll
-      for (int rb = 0; rb < RG; ++rb) fr[0][rb] = frag(st, rb, g);
+      for (int r = 0; r < RG; ++r) fr[0][r] = frag(st, r, g);
 #pragma unroll
-      for (int rb = 0; rb < R; ++rb)
-        sa[rb] = *(const int*)(scl + (b * BM + 16 * rb + m) * 16 + 4 * g);
+      for (int rb = 0; rb < RB; ++rb) read_scales(scl + (b * BM + MS * rb + m) * 16, sa[rb]);
       if constexpr (more) {
         load_ws(No{}, c + 1);     // before the codes: the waits for these leave them in flight
         load_a(No{}, c + 1);
       }
       each4([&](auto J) {
         constexpr int j = decltype(J)::value;
-        advance_w(AHEAD, J, c);
+        // with several groups a slice the writes to LDS come behind its first
+        if constexpr (NG == 1 || j % 2 == 0) advance_w(AHEAD, J, c);
+        each<NG>([&](auto I) {
+          constexpr int u = decltype(I)::value / NH, h = decltype(I)::value % NH;
+          constexpr int n = j * NG + decltype(I)::value;
+          if constexpr (decltype(I)::value == 1) {
+            if constexpr (j % 2 == 1) advance_w(AHEAD, J, c);
+            if constexpr (more && j == 3) write_a(c + 1);
+          }
+          if (opaque(1)) {
+            if constexpr (n + 1 < 4 * NG) {
+              constexpr int j1 = (n + 1) / NG, u1 = (n + 1) % NG / NH, h1 = (n + 1) % NH;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const int n = j * NH + h;
-          if (opaque()) {
-            if (n + 1 < 4 * NH) {
-#pragma unroll
-              for (int rb = 0; rb < RG; ++rb)
-                fr[(n + 1) & 1][rb] =
-                    frag(st, ((n + 1) % NH) * RG + rb, 4 * ((n + 1) / NH) + g);
+              for (int r = 0; r < RG; ++r)
+                fr[(n + 1) & 1][r] = frag(st, h1 * RG + r, 4 * j1 + G * u1 + g);
             }
 #pragma unroll
             for (int r = 0; r < RG; ++r) {
               const i32x4 f = fr[n & 1][r];
               const i32x8 fa = {f[0], f[1], f[2], f[3], 0, 0, 0, 0};
+              constexpr int w0 = kDword(j);
               const int rb = h * RG + r;
 #pragma unroll
-              for (int cb = 0; cb < CB; ++cb) {
-                const i32x4 w = fw[j & 1][cb];
+              for (int b = 0; b < NB; ++b) {
+                const i32x4 w = fw[j & 1][b][u];
                 const i32x8 fb = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
-                acc[rb][cb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    fb, fa, acc[rb][cb], kFp4, kFp4, j, sw[cb], j, sa[rb]);
+                acc[rb][b] = M::template fp4<kByte(j, u)>(fb, fa, acc[rb][b], sw[b][w0], sa[rb][w0]);
               }
             }
           }
-        }
+        });
       });
       if constexpr (more) {
-        write_a(c + 1);
+        if constexpr (NG == 1) write_a(c + 1);
         pass_scales();
       }
       lds_barrier();
@@ -374,6 +454,7 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     lds_barrier();
     sweep(chunk);
   } else {
+    constexpr int NG = 4 * U * NH;       // groups per slice
     constexpr int PA = R <= 2 ? 4 : 2;   // row stages in flight in registers
     i32x4 av[PA][R];
     const int S = 4 * KC;
@@ -382,53 +463,49 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
 #pragma unroll
       for (int i = 0; i < R; ++i) v[i] = *(const i32x4*)(row_ptr(i) + kb);
     };
-    auto compute = [&](auto J) {
+    // slice J; between(n) runs behind group n.  !live: only those
+    auto compute = [&](auto J, int live, auto&& between) {
       constexpr int j = decltype(J)::value;
       const char* st = smem + (j & 1) * stage_bytes;
-      float sc2[CB];
-      bf16x8 fb[2][CB];
-      // e8m0 byte as an fp32 power of two (0xFF: NaN)
+      bf16x8 fb[2][NB];
+      // codes of fragment q in instruction u as bf16, scaled (0xFF: NaN)
+      auto unpack = [&](auto Q) {
+        constexpr int u = decltype(Q)::value / 4, q = decltype(Q)::value % 4;
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-        sc2[cb] = __uint_as_float(__builtin_amdgcn_ubfe((unsigned)sw[cb], 8 * j, 8) << 23);
-      auto unpack = [&](bf16x8* o, int q) {
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          const unsigned u = (unsigned)fw[j & 1][cb][q];
-          const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 0);
-          const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 1);
-          const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 2);
-          const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, sc2[cb], 3);
-          o[cb] = bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+        for (int b = 0; b < NB; ++b) {
+          const float s2 = __uint_as_float(
+              __builtin_amdgcn_ubfe((unsigned)sw[b][kDword(j)], 8 * kByte(j, u), 8) << 23);
+          const unsigned c = (unsigned)fw[j & 1][b][u][q];
+          const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s2, 0);
+          const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s2, 1);
+          const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s2, 2);
+          const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s2, 3);
+          fb[q & 1][b] = bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
         }
       };
 #pragma unroll
-      for (int rb = 0; rb < RG; ++rb) fr[0][rb] = frag(st, rb, 4 * g);
-      unpack(fb[0], 0);
+      for (int r = 0; r < RG; ++r) fr[0][r] = frag(st, r, g);
+      unpack(C<0>{});
+      each<NG>([&](auto I) {
+        constexpr int n = decltype(I)::value, uq = n / NH, q = uq % 4, h = n % NH;
+        if (opaque(live)) {
+          if constexpr (n + 1 < NG) {
+            constexpr int u1 = (n + 1) / NH / 4, q1 = (n + 1) / NH % 4, h1 = (n + 1) % NH;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+            for (int r = 0; r < RG; ++r)
+              fr[(n + 1) & 1][r] = frag(st, h1 * RG + r, 4 * q1 + G * u1 + g);
+          }
+          if constexpr (h == NH - 1 && uq + 1 < 4 * U) unpack(C<uq + 1>{});
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const int n = q * NH + h;
-          if (opaque()) {
-            if (n + 1 < 4 * NH) {
+          for (int r = 0; r < RG; ++r) {
+            const bf16x8 fa = __builtin_bit_cast(bf16x8, fr[n & 1][r]);
+            const int rb = h * RG + r;
 #pragma unroll
-              for (int rb = 0; rb < RG; ++rb)
-                fr[(n + 1) & 1][rb] =
-                    frag(st, ((n + 1) % NH) * RG + rb, 4 * g + (n + 1) / NH);
-            }
-            if (h == NH - 1 && q < 3) unpack(fb[(q + 1) & 1], q + 1);
-#pragma unroll
-            for (int r = 0; r < RG; ++r) {
-              const bf16x8 fa = __builtin_bit_cast(bf16x8, fr[n & 1][r]);
-              const int rb = h * RG + r;
-#pragma unroll
-              for (int cb = 0; cb < CB; ++cb)
-                acc[rb][cb] =
-                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q & 1][cb], fa, acc[rb][cb], 0, 0, 0);
-            }
+            for (int b = 0; b < NB; ++b) acc[rb][b] = M::bf16_(fb[q & 1][b], fa, acc[rb][b]);
           }
         }
+        between(I);
+      });
     };
     auto chunk = [&](auto AHEAD, int c) {
       constexpr bool more = decltype(AHEAD)::value > 0;
@@ -437,15 +514,23 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
       each4([&](auto J) {
         constexpr int j = decltype(J)::value;
         const int s = 4 * c + j;
-        if constexpr (more || j < 3) {
-          i32x4* v = av[(j + 1) % PA];
-          write_rows(smem + ((j + 1) & 1) * stage_bytes, v);
-          if constexpr (more || j + 1 + PA < 4) load_a(v, min(s + 1 + PA, S - 1));
+        auto rows_on = [&] {
+          if constexpr (more || j < 3) {
+            i32x4* v = av[(j + 1) % PA];
+            write_rows(smem + ((j + 1) & 1) * stage_bytes, v);
+            if constexpr (more || j + 1 + PA < 4) load_a(v, min(s + 1 + PA, S - 1));
+          }
+        };
+        if constexpr (RB == 1) {
+          rows_on();
+          advance_w(AHEAD, J, c);
         }
-        advance_w(AHEAD, J, c);
         // not the slices that the chunk before holds, nor those past a short row
         const int k = k0 + 128 * j;
-        if (k >= c * kChunk && k < D) compute(J);
+        compute(J, k >= c * kChunk && k < D ? 1 : 0, [&](auto I) {
+          if constexpr (RB > 1 && decltype(I)::value == 0) rows_on();
+          if constexpr (RB > 1 && decltype(I)::value == 1) advance_w(AHEAD, J, c);
+        });
         if constexpr (more && j == 3) pass_scales();
         lds_barrier();
       });
@@ -460,21 +545,25 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     sweep(chunk);
   }
 
-  // ---- lane l: row 16 rb + l % 16, output columns col0 + 4 CBH g + [0, 4 CBH)
-  const int n0 = col0 + 4 * CBH * g;
-  if (n0 >= width) return;
+  // ---- lane l: row MS rb + l % MS, SL outputs (SwiGLU: SL / 2) from column n0
+  constexpr int OC = SW ? SL / 2 : SL;
+  const int n0 = col0 + OC * g;
 #pragma unroll
-  for (int rb = 0; rb < R; ++rb) {
-    const int r = 16 * rb + m;
+  for (int rb = 0; rb < RB; ++rb) {
+    const int r = MS * rb + m;
     if (r >= rows) continue;
-    float v[4 * CBH];
+    auto at = [&](int slot) { return acc[rb][slot / kAcc][slot % kAcc]; };
 #pragma unroll
-    for (int h = 0; h < CBH; ++h)
+    for (int i = 0; i < OC; i += 4) {
+      // whole groups of 8 columns where a lane has them; widths are even
+      // multiples of 8, so that none is split
+      constexpr int W = OC % 8 == 0 ? 8 : 4;
+      if (i % W) continue;
+      float v[W];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        v[4 * h + q] = SW ? silu(acc[rb][h][q]) * acc[rb][CBH + (SW ? h : 0) - (SW ? 0 : CBH)][q]
-                          : acc[rb][h][q];
-    store_cols<OutT, 4 * CBH>((OutT*)p.out + (size_t)(row0 + r) * width + n0, v);
+      for (int k = 0; k < W; ++k) v[k] = SW ? silu(at(i + k)) * at(OC + i + k) : at(i + k);
+      if (n0 + i < width) store_cols<OutT, W>((OutT*)p.out + (size_t)(row0 + r) * width + n0 + i, v);
+    }
   }
 }
 
@@ -514,7 +603,7 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_small(GemmArgs p) {
     // nothing of a turn is kept in registers for the next
     int e = __builtin_amdgcn_readfirstlane(t.x), n = __builtin_amdgcn_readfirstlane(nt);
     asm volatile("" : "+s"(e), "+s"(n));
-    tile<1, CB, A4, SW, true, OutT>(smem, p, e, t.y + r, min(kSmallRows, t.z - r), n);
+    tile<16, 1, CB, A4, SW, true, OutT>(smem, p, e, t.y + r, min(kSmallRows, t.z - r), n);
     r += kSmallRows;
   } while (r < t.z);
 }
@@ -529,9 +618,9 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_mid(GemmArgs p) {
   int nt;
   if (!find_tile(p, t, nt)) return;
   if (t.z <= 32)
-    tile<2, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
+    tile<32, 1, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
   else
-    tile<4, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
+    tile<32, 2, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
 }
 
 // 65 to kMaxRows rows
@@ -541,13 +630,15 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_large(GemmArgs p) {
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
-  if constexpr (!A4) {
-    tile<8, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
-  } else {
-    if (t.z <= 128)
-      tile<8, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
+  if (t.z <= 96)
+    tile<32, 3, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if (!A4 || t.z <= 128)
+    tile<32, 4, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if constexpr (A4) {
+    if (t.z <= 160)
+      tile<32, 5, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
     else
-      tile<12, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
+      tile<32, 6, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
   }
 }
 
