@@ -8,7 +8,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DT, _I, _P, _check, _dev, _ptr, _require, _stream, _want, lib
+from . import _DT, _I, _P, _check, _dev, _require, _want, lib
 
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
@@ -25,6 +25,25 @@ SIGS = {
     "moe_norm": ([_P, _I, _P, _F, _I, _I, _P, _I, _P], _I),
     "moe_norm_residual": ([_P, _I, _P, _F, _P, _I, _F, _P, _I, _P, _P, _P, _I, _I, _P], _I),
 }
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, device, *args):
+    """The C call `name` on the device's current stream, with the device current.
+    One call of a decode step costs the host as long as its kernel runs, so the
+    way there is short: plain integers for pointers, the stream's handle without
+    a Stream object around it, no device switch where there is none to make."""
+    f = getattr(lib(), name)
+    i = device.index
+    if i == torch.cuda.current_device():
+        _check(name, f(*args, torch._C._cuda_getCurrentRawStream(i)))
+    else:
+        with torch.cuda.device(i):
+            _check(name, f(*args, torch._C._cuda_getCurrentRawStream(i)))
+
 
 BLOCK = 32                     # values that share a scale
 GATES = {"none": 0, "channel": 1, "token": 2}
@@ -45,11 +64,11 @@ class MXFP4(NamedTuple):
 def _mx(codes, scales, name):
     """Shape (rows..., cols) of a pair of codes and scales."""
     _want(codes, torch.uint8, name)
-    _want(scales, torch.uint8, name + " scales")
-    cols = 2 * codes.shape[-1]
-    _require(cols % BLOCK == 0 and scales.shape == (*codes.shape[:-1], cols // BLOCK),
-             f"{name}: codes [..., C / 2] and scales [..., C / 32]")
-    return (*codes.shape[:-1], cols)
+    _want(scales, torch.uint8, name)
+    *rows, half = codes.shape
+    _require(half % (BLOCK // 2) == 0 and scales.shape == (*rows, half // (BLOCK // 2)),
+             "codes [..., C / 2] and scales [..., C / 32]")
+    return (*rows, 2 * half)
 
 
 def moe_mxfp4_quantize(x, codes, scales, n_rows=None):
@@ -61,10 +80,8 @@ def moe_mxfp4_quantize(x, codes, scales, n_rows=None):
     if n_rows is not None:
         _want(n_rows, torch.int32, "n_rows")
         _require(n_rows.numel() >= 1, "n_rows.numel() >= 1")
-    with torch.cuda.device(d):
-        _check("moe_mxfp4_quantize", lib().moe_mxfp4_quantize(
-            _ptr(x), _DT[x.dtype], x.numel() // max(cols, 1), cols, _ptr(n_rows), _ptr(codes),
-            _ptr(scales), _stream(x)))
+    _call("moe_mxfp4_quantize", d, _p(x), _DT[x.dtype], x.numel() // max(cols, 1), cols,
+          _p(n_rows), _p(codes), _p(scales))
 
 
 def moe_mxfp4_dequantize(codes, scales, y):
@@ -72,10 +89,8 @@ def moe_mxfp4_dequantize(codes, scales, y):
     d = _dev(codes, scales, y)
     _require(_mx(codes, scales, "codes") == tuple(y.shape), "codes and scales of y's shape")
     cols = y.shape[-1]
-    with torch.cuda.device(d):
-        _check("moe_mxfp4_dequantize", lib().moe_mxfp4_dequantize(
-            _ptr(codes), _ptr(scales), _DT[y.dtype], y.numel() // max(cols, 1), cols, _ptr(y),
-            _stream(y)))
+    _call("moe_mxfp4_dequantize", d, _p(codes), _p(scales), _DT[y.dtype],
+          y.numel() // max(cols, 1), cols, _p(y))
 
 
 def quantize_weights(w):
@@ -116,11 +131,9 @@ def moe_grouped_gemm_mxfp4(a, a_scales, offsets, w, w_scales, out, ws, row_src=N
     else:
         _want(row_src, torch.int32, "row_src")
         _require(row_src.numel() >= rows_cap, "row_src.numel() >= out.shape[0]")
-    with torch.cuda.device(d):
-        _check("moe_grouped_gemm_mxfp4", lib().moe_grouped_gemm_mxfp4(
-            _ptr(a), _ptr(a_scales), _ptr(row_src), a.shape[0], K, _ptr(offsets), rows_cap, E, D,
-            N, _ptr(w), _ptr(w_scales), 1 if swiglu else 0, _DT[out.dtype], _ptr(out), _ptr(ws),
-            ws.numel() * ws.element_size(), _stream(a)))
+    _call("moe_grouped_gemm_mxfp4", d, _p(a), _p(a_scales), _p(row_src), a.shape[0], K,
+          _p(offsets), rows_cap, E, D, N, _p(w), _p(w_scales), 1 if swiglu else 0,
+          _DT[out.dtype], _p(out), _p(ws), ws.numel() * ws.element_size())
 
 
 def moe_expert_ffn_mxfp4_workspace_bytes(rows_cap, n_ffn, I):
@@ -148,17 +161,15 @@ def moe_expert_ffn_mxfp4(x, x_scales, K, row_src, offsets, w13, w13_scales, w2, 
     _require(y_perm.shape == (rows_cap, H) and row_src.numel() >= rows_cap,
              "y_perm of H columns and row_src.numel() >= rows_cap")
     _require(offsets.numel() >= N + 1, "offsets.numel() >= n_ffn + 1")
-    with torch.cuda.device(d):
-        _check("moe_expert_ffn_mxfp4", lib().moe_expert_ffn_mxfp4(
-            _ptr(x), _ptr(x_scales), x.shape[0], K, _ptr(row_src), _ptr(offsets), rows_cap, N, H,
-            I, _ptr(w13), _ptr(w13_scales), _ptr(w2), _ptr(w2_scales), _ptr(y_perm), _ptr(ws),
-            ws.numel() * ws.element_size(), _stream(x)))
+    _call("moe_expert_ffn_mxfp4", d, _p(x), _p(x_scales), x.shape[0], K, _p(row_src),
+          _p(offsets), rows_cap, N, H, I, _p(w13), _p(w13_scales), _p(w2), _p(w2_scales),
+          _p(y_perm), _p(ws), ws.numel() * ws.element_size())
 
 
 def _norm_weight(w, H, name):
     if w is not None:
         _want(w, torch.float32, name)
-        _require(w.shape == (H,), f"{name}.shape == (H,)")
+        _require(w.shape == (H,), name)
 
 
 def moe_norm(x, weight, y, eps=1e-5):
@@ -168,9 +179,7 @@ def moe_norm(x, weight, y, eps=1e-5):
     T, H = x.shape
     _norm_weight(weight, H, "weight")
     _require(y.shape == (T, H), "y.shape == x.shape")
-    with torch.cuda.device(d):
-        _check("moe_norm", lib().moe_norm(_ptr(x), _DT[x.dtype], _ptr(weight), float(eps), T, H,
-                                          _ptr(y), _DT[y.dtype], _stream(x)))
+    _call("moe_norm", d, _p(x), _DT[x.dtype], _p(weight), eps, T, H, _p(y), _DT[y.dtype])
 
 
 def moe_norm_residual(y, residual, out, scale=1.0, w_post=None, gate=None, gate_kind="none",
@@ -194,11 +203,9 @@ def moe_norm_residual(y, residual, out, scale=1.0, w_post=None, gate=None, gate_
     if next_out is not None:
         _want(next_out, y.dtype, "next_out")
         _require(next_out.shape == (T, H), "next_out.shape == y.shape")
-    with torch.cuda.device(d):
-        _check("moe_norm_residual", lib().moe_norm_residual(
-            _ptr(y), _DT[y.dtype], _ptr(w_post), float(eps), _ptr(gate), GATES[gate_kind],
-            float(scale), _ptr(residual), _DT[residual.dtype], _ptr(out), _ptr(w_next),
-            _ptr(next_out), T, H, _stream(y)))
+    _call("moe_norm_residual", d, _p(y), _DT[y.dtype], _p(w_post), eps, _p(gate),
+          GATES[gate_kind], scale, _p(residual), _DT[residual.dtype], _p(out), _p(w_next),
+          _p(next_out), T, H)
 
 
 def block_forward(h, w_norm, w_router, bias, w13, w2, K, ffn_scale, buf, scale=1.0, w_post=None,
