@@ -48,8 +48,7 @@ constexpr int kChunk = 512;        // values of a weight row per load chunk
 // bound an expert of more than about 100 rows, and 256 rows' accumulators next
 // to the fragments in two forms do not fit the registers.
 template <bool A4> constexpr int kMaxRows = A4 ? 192 : 128;
-constexpr int kSmallRows = 16;     // m-tiles of the small kernel
-constexpr int kMidRows = 64;       // ... and of the middle one
+constexpr int kFewRows = 16;       // rows of a decode m-tile
 using Yes = std::true_type;
 using No = std::false_type;
 template <int I> using C = std::integral_constant<int, I>;
@@ -72,10 +71,10 @@ struct GemmArgs {
   const uint8_t* w;                // [E][N][D / 2]
   const uint8_t* w_scales;         // [E][N][D / 32]
   void* out;                       // [.][N] or, SwiGLU, [.][N / 2]
-  // list mode: m-tiles tiles[span[0]] .. tiles[span[1] - 1]; direct mode (span
-  // NULL): m-tile number e is expert e's rows
+  // list mode: m-tiles tiles[0] .. tiles[*count - 1]; direct mode (count NULL):
+  // the rows of each expert that has any
   const int4* tiles;
-  const int* span;
+  const int* count;
   int NT;                          // column tiles
 };
 
@@ -206,7 +205,11 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
 #pragma unroll
   for (int i = 0; i < NL; ++i)
     woff[i] = weight_row(8 * i + (lane >> 3)) * (uint32_t)code_pitch;
-  const uint32_t soff = weight_row(lane & (16 * CB - 1)) * (uint32_t)scale_pitch;
+  constexpr int NS = (16 * CB + 63) / 64;       // scale rows of a lane
+  uint32_t soff[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i)
+    soff[i] = weight_row((lane & (16 * CB - 1)) + 64 * i) * (uint32_t)scale_pitch;
   // Loads in front of the loop also take rows shorter than a chunk (FIRST): the
   // same places again instead of bytes past the row.  Loads inside the loop do
   // not branch, so that the waits for them stay exact.
@@ -218,7 +221,7 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     for (int j = 0; j < 4; ++j) v[j] = *(const int*)(s + 4 * min(j, last_j));
     return v;
   };
-  i32x4 wr[2][NL], wsr;                          // steps in flight; the next chunk's scales
+  i32x4 wr[2][NL], wsr[NS];                      // steps in flight; the next chunk's scales
   auto load_w = [&](auto FIRST, auto B, int step) {
     constexpr int b = decltype(B)::value;        // step & 1
     const int at = 128 * b + 16 * (lane & 7);    // in the chunk
@@ -230,7 +233,10 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
       wr[b][i] = NT ? __builtin_nontemporal_load(src) : *src;
     }
   };
-  auto load_ws = [&](auto FIRST, int c) { wsr = load_scales(FIRST, sbase + soff, window(c)); };
+  auto load_ws = [&](auto FIRST, int c) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) wsr[i] = load_scales(FIRST, sbase + soff[i], window(c));
+  };
   char* wlds = smem + 2 * BM * kPitch + (A4 ? 2 * BM * 16 : 0) + wave * kWaveLds<CB>;
   char* slds = wlds + 16 * CB * 128;
   auto write_w = [&](auto B) {
@@ -279,7 +285,10 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   };
   int sw[NB][U];
   auto pass_scales = [&] {
-    if (16 * CB == 64 || lane < 16 * CB) *(i32x4*)(slds + lane * 16) = scale_dwords(wsr);
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (16 * CB >= 64 || lane < 16 * CB)
+        *(i32x4*)(slds + (lane + 64 * i) * 16) = scale_dwords(wsr[i]);
 #pragma unroll
     for (int b = 0; b < NB; ++b) read_scales(slds + (MS * b + m) * 16, sw[b]);
   };
@@ -466,7 +475,7 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
     sweep(chunk);
   } else {
     constexpr int NG = 4 * U * NH;       // groups per slice
-    constexpr int PA = R <= 2 ? 4 : 2;   // row stages in flight in registers
+    constexpr int PA = 2;                // row stages in flight in registers
     i32x4 av[PA][R];
     const int S = 4 * KC;
     auto load_a = [&](i32x4* v, int s) {
@@ -585,26 +594,42 @@ __device__ __forceinline__ bool find_tile(const GemmArgs& p, int4& t, int& nt) {
   const int b = blockIdx.x, slot = b >> 3;
   const int mt = (slot / p.NT) * 8 + (b & 7);
   nt = slot % p.NT;
-  if (p.span) {
-    const int at = p.span[0] + mt;
-    if (at >= p.span[1]) return false;
-    t = p.tiles[at];
+  if (p.count) {
+    if (mt >= *p.count) return false;
+    t = p.tiles[mt];
     return true;
   }
-  if (mt >= p.n_experts) return false;
-  const int r0 = min(max(p.offsets[mt], 0), p.rows_cap);
-  const int n = min(max(p.offsets[mt + 1], r0), p.rows_cap) - r0;
-  t = make_int4(mt, r0, n, 1);
-  return n > 0;
+  // the mt-th of the experts that have rows, 64 experts a turn (numbered
+  // without the others, m-tiles spread over the XCDs evenly)
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 < p.n_experts; e0 += 64) {
+    const int e = e0 + lane;
+    int r0 = 0, m = 0;
+    if (e < p.n_experts) {
+      r0 = min(max(p.offsets[e], 0), p.rows_cap);
+      m = min(max(p.offsets[e + 1], r0), p.rows_cap) - r0;
+    }
+    const unsigned long long hit = __ballot(m > 0);
+    const int k = mt - before;
+    before += __popcll(hit);
+    if (mt < before) {
+      const bool mine = m > 0 && __popcll(hit & ((1ull << lane) - 1)) == k;
+      const int src = __ffsll((long long)__ballot(mine)) - 1;
+      t = make_int4(e0 + src, __builtin_amdgcn_readlane(r0, src),
+                    __builtin_amdgcn_readlane(m, src), 0);
+      return true;
+    }
+  }
+  return false;
 }
 
-// Three kernels by the m-tile's rows, since a kernel's registers are those of
-// its largest tile: with one of 32 rows beside it, that of 16 spilled.
+// Two kernels, since a kernel's registers are those of its largest tile.
 //
-// At most 16 rows.  Direct mode is taken where no dispatch gives an expert
-// more; one that has more all the same is taken 16 rows at a time.
+// Few rows an expert (decode): every m-tile is one of at most 16 rows, two
+// blocks to a CU.  An expert that has more is taken 16 rows at a time.
 template <int CB, bool A4, bool SW, typename OutT>
-__global__ __launch_bounds__(kThreads, 2) void gemm_small(GemmArgs p) {
+__global__ __launch_bounds__(kThreads, 2) void gemm_few(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) char smem[lds_bytes<1, CB, A4>()];
   int4 t;
   int nt;
@@ -614,34 +639,27 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_small(GemmArgs p) {
     // nothing of a turn is kept in registers for the next
     int e = __builtin_amdgcn_readfirstlane(t.x), n = __builtin_amdgcn_readfirstlane(nt);
     asm volatile("" : "+s"(e), "+s"(n));
-    tile<16, 1, CB, A4, SW, true, OutT>(smem, p, e, t.y + r, min(kSmallRows, t.z - r), n);
-    r += kSmallRows;
+    tile<16, 1, CB, A4, SW, true, OutT>(smem, p, e, t.y + r, min(kFewRows, t.z - r), n);
+    r += kFewRows;
   } while (r < t.z);
 }
 
-// 17 to 64 rows, two column blocks a wave, so that the fragments
-// in both forms fit the registers of two blocks per CU.
-constexpr int kMidCB = 2;
+// m-tiles of any size up to kMaxRows, one block to a CU.  One launch for all of
+// them: with one each for up to 16, up to 64 and more rows, the few m-tiles of
+// the rarer sizes held the chip by themselves (50 rows an expert: FFN 462 us).
 template <bool A4, bool SW, typename OutT>
-__global__ __launch_bounds__(kThreads, 2) void gemm_mid(GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char smem[lds_bytes<4, kMidCB, A4>()];
-  int4 t;
-  int nt;
-  if (!find_tile(p, t, nt)) return;
-  if (t.z <= 32)
-    tile<32, 1, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
-  else
-    tile<32, 2, kMidCB, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
-}
-
-// 65 to kMaxRows rows
-template <bool A4, bool SW, typename OutT>
-__global__ __launch_bounds__(kThreads, 1) void gemm_large(GemmArgs p) {
+__global__ __launch_bounds__(kThreads, 1) void gemm_any(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) char smem[lds_bytes<kMaxRows<A4> / 16, 4, A4>()];
   int4 t;
   int nt;
   if (!find_tile(p, t, nt)) return;
-  if (t.z <= 96)
+  if (t.z <= 16)
+    tile<16, 1, 4, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if (t.z <= 32)
+    tile<32, 1, 4, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if (t.z <= 64)
+    tile<32, 2, 4, A4, SW, true, OutT>(smem, p, t.x, t.y, t.z, nt);
+  else if (t.z <= 96)
     tile<32, 3, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
   else if (!A4 || t.z <= 128)
     tile<32, 4, 4, A4, SW, false, OutT>(smem, p, t.x, t.y, t.z, nt);
@@ -653,46 +671,39 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_large(GemmArgs p) {
   }
 }
 
-// Launches of one kind of rows.  kind 0: the small kernel, with cb column
-// blocks per wave (4, 2 and, without SwiGLU, 1); 1: the middle one; 2: the large.
+// Launches of one form of rows.  few_cb: 0, gemm_any over the m-tile list; 2 or
+// (without SwiGLU) 1, gemm_few with so many column blocks a wave.
 template <bool A4>
-hipError_t launch_gemm(GemmArgs p, int kind, bool swiglu, int out_dtype, int cb, unsigned mtiles,
+hipError_t launch_gemm(GemmArgs p, int few_cb, bool swiglu, int out_dtype, unsigned mtiles,
                        hipStream_t s);
 
 template <bool A4, bool SW, typename OutT>
-void launch_gemm_t(GemmArgs& p, int kind, int cb, unsigned mtiles, hipStream_t s) {
-  const int width = SW ? p.N / 2 : p.N;
-  if (kind == 1) cb = kMidCB;
+void launch_gemm_t(GemmArgs& p, int few_cb, unsigned mtiles, hipStream_t s) {
+  const int width = SW ? p.N / 2 : p.N, cb = few_cb ? few_cb : 4;
   p.NT = (int)ceil_div(width, SW ? 32 * cb : 64 * cb);
   const unsigned grid = ceil_div(mtiles, 8) * 8 * p.NT;
-  if (kind == 2) {
-    MOE_LAUNCH(A4 ? "mx_gemm_large_fp4" : "mx_gemm_large_bf16", s,
-               gemm_large<A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
-  } else if (kind == 1) {
-    MOE_LAUNCH(A4 ? "mx_gemm_mid_fp4" : "mx_gemm_mid_bf16", s,
-               gemm_mid<A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
-  } else if (cb == 4) {
-    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
-               gemm_small<4, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
-  } else if (cb == 2) {
-    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
-               gemm_small<2, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  if (few_cb == 0) {
+    MOE_LAUNCH(A4 ? "mx_gemm_any_fp4" : "mx_gemm_any_bf16", s,
+               gemm_any<A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+  } else if (few_cb == 2) {
+    MOE_LAUNCH(A4 ? "mx_gemm_few_fp4" : "mx_gemm_few_bf16", s,
+               gemm_few<2, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
   } else if constexpr (!SW) {
-    MOE_LAUNCH(A4 ? "mx_gemm_small_fp4" : "mx_gemm_small_bf16", s,
-               gemm_small<1, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
+    MOE_LAUNCH(A4 ? "mx_gemm_few_fp4" : "mx_gemm_few_bf16", s,
+               gemm_few<1, A4, SW, OutT><<<grid, kThreads, 0, s>>>(p));
   }
 }
 
 #define MX_INSTANTIATE(A4)                                                                       \
   template <>                                                                                    \
-  hipError_t launch_gemm<A4>(GemmArgs p, int kind, bool swiglu, int out_dtype, int cb,           \
+  hipError_t launch_gemm<A4>(GemmArgs p, int few_cb, bool swiglu, int out_dtype,                 \
                              unsigned mtiles, hipStream_t s) {                                   \
     if (out_dtype == MOE_BF16)                                                                   \
-      swiglu ? launch_gemm_t<A4, true, bf16>(p, kind, cb, mtiles, s)                             \
-             : launch_gemm_t<A4, false, bf16>(p, kind, cb, mtiles, s);                           \
+      swiglu ? launch_gemm_t<A4, true, bf16>(p, few_cb, mtiles, s)                               \
+             : launch_gemm_t<A4, false, bf16>(p, few_cb, mtiles, s);                             \
     else                                                                                         \
-      swiglu ? launch_gemm_t<A4, true, float>(p, kind, cb, mtiles, s)                            \
-             : launch_gemm_t<A4, false, float>(p, kind, cb, mtiles, s);                          \
+      swiglu ? launch_gemm_t<A4, true, float>(p, few_cb, mtiles, s)                              \
+             : launch_gemm_t<A4, false, float>(p, few_cb, mtiles, s);                            \
     return hipGetLastError();                                                                    \
   }
 

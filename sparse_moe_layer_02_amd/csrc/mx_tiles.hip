@@ -14,18 +14,24 @@ constexpr size_t kHeader = 256;
 inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 // m-tiles of bm rows at most; workspaces hold the list of either form of rows
 inline int tile_rows(bool fp4_rows) { return fp4_rows ? kMaxRows<true> : kMaxRows<false>; }
+// Whether the experts have few rows each: no expert more than 16, or on average
+// at most 8 and none over 128 (one that does have many is read once for every
+// 16 rows, which costs less than the list, about 10 us a call).
+inline bool few_rows(int rows_cap, int n_experts, int rows_max) {
+  return rows_max <= kFewRows || (rows_max <= 128 && (long long)rows_cap <= 8ll * n_experts);
+}
 inline size_t max_tiles(int rows_cap, int n_experts, int bm) {
   return (size_t)rows_cap / bm + n_experts;
 }
 
-// The m-tiles of all experts, those of more than 64 rows first, then those of
-// 17 to 64, then the rest; head[0..3]: where each part starts and the last
-// ends.  An expert of m rows has m / bm full m-tiles and a rest.  Rows are
-// clamped to [0, rows_cap) and the list to its capacity, so malformed offsets
-// shrink the work but never index past the buffers.
+// The m-tiles of all experts, the largest first so that the small ones fill the
+// end: those of more than 64 rows, of 17 to 64, and the rest; *count: how many.
+// An expert of m rows has m / bm full m-tiles and a rest.  Rows are clamped to
+// [0, rows_cap) and the list to its capacity, so malformed offsets shrink the
+// work but never index past the buffers.
 __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restrict__ offsets,
                                                          int n_experts, int rows_cap, int bm,
-                                                         int max_tiles, int* __restrict__ head,
+                                                         int max_tiles, int* __restrict__ count,
                                                          int4* __restrict__ tiles) {
   constexpr int kParts = 3;
   __shared__ int wave_sum[kParts][kListThreads / kWave];
@@ -36,7 +42,7 @@ __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restri
     r0 = min(max(offsets[e], 0), rows_cap);
     m = min(max(offsets[e + 1], r0), rows_cap) - r0;
   };
-  auto part_of = [](int rows) { return rows > kMidRows ? 0 : rows > kSmallRows ? 1 : 2; };
+  auto part_of = [](int rows) { return rows > 64 ? 0 : rows > 16 ? 1 : 2; };
   int mine[kParts] = {0, 0, 0}, sum[kParts];
   for (int e = lo; e < hi; ++e) {
     int r0, m;
@@ -65,10 +71,9 @@ __global__ __launch_bounds__(kListThreads) void mx_tiles(const int32_t* __restri
       all += wave_sum[i][w];
     }
     at[i] = start + before + sum[i] - mine[i];
-    if (tid == 0) head[i] = start;
     start = end[i] = min(start + all, max_tiles);
   }
-  if (tid == 0) head[kParts] = start;
+  if (tid == 0) *count = start;
   for (int e = lo; e < hi; ++e) {
     int r0, m;
     span(e, r0, m);
@@ -98,7 +103,7 @@ bool grid_fits(int rows_cap, int n_experts, int N) {
 hipError_t launch_tiles(const int32_t* offsets, int rows_cap, int n_experts, int rows_max,
                         bool fp4_rows, void* ws, hipStream_t s) {
   const int bm = tile_rows(fp4_rows);
-  if (rows_max <= kSmallRows) return hipSuccess;   // one m-tile an expert, found by its number
+  if (few_rows(rows_cap, n_experts, rows_max)) return hipSuccess;   // found by every block itself
   MOE_LAUNCH("mx_tiles", s,
              mx_tiles<<<1, kListThreads, 0, s>>>(offsets, n_experts, rows_cap, bm,
                                                  (int)max_tiles(rows_cap, n_experts, bm), (int*)ws,
@@ -125,30 +130,20 @@ hipError_t launch_product(const void* a, const uint8_t* a_scales, const int32_t*
   p.w_scales = w_scales;
   p.out = out;
   const bool fp4 = a_scales != nullptr;
-  auto launch = [&](int kind, int cb, size_t mtiles) {
-    return fp4 ? launch_gemm<true>(p, kind, swiglu, out_dtype, cb, (unsigned)mtiles, s)
-               : launch_gemm<false>(p, kind, swiglu, out_dtype, cb, (unsigned)mtiles, s);
-  };
-  const size_t E = (size_t)n_experts, cap = (size_t)rows_cap;
-  hipError_t e = hipSuccess;
-  if (rows_max > kSmallRows) {
-    const int* head = (const int*)ws;
+  int few_cb = 0;
+  size_t mtiles = max_tiles(rows_cap, n_experts, tile_rows(fp4));
+  if (few_rows(rows_cap, n_experts, rows_max)) {
+    mtiles = (size_t)std::min(rows_cap, n_experts);   // experts with rows, at most
+    // 128 weight rows a block (two 16-row blocks a wave) where that gives every
+    // CU its two, else 64.  256 rows a block were slower at every size (decode
+    // FFN 189 against 167 us): fewer blocks to even out over the CUs.
+    few_cb = swiglu || mtiles * ceil_div(N, 128) >= 512 ? 2 : 1;
+  } else {
     p.tiles = (const int4*)((char*)ws + kHeader);
-    // grids by what the rows allow at most: a part's m-tiles hold so many rows
-    // each, and an expert has one m-tile that is not full
-    if (rows_max > kMidRows) {
-      p.span = head;
-      e = launch(2, 4, std::min(cap / (kMidRows + 1), cap / tile_rows(fp4) + E));
-    }
-    p.span = head + 1;
-    if (e == hipSuccess) e = launch(1, 4, std::min(cap / (kSmallRows + 1), E));
-    if (e != hipSuccess) return e;
-    p.span = head + 2;
+    p.count = (const int*)ws;
   }
-  const size_t hit = std::min(cap, E);           // experts with rows, at most
-  const size_t blocks4 = hit * ceil_div(N, 256);
-  const int cb = blocks4 >= 512 ? 4 : 2 * blocks4 >= 512 || swiglu ? 2 : 1;
-  return launch(0, cb, p.span ? hit : E);
+  return fp4 ? launch_gemm<true>(p, few_cb, swiglu, out_dtype, (unsigned)mtiles, s)
+             : launch_gemm<false>(p, few_cb, swiglu, out_dtype, (unsigned)mtiles, s);
 }
 
 }  // namespace mx
