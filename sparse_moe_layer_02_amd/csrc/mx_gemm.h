@@ -87,10 +87,11 @@ __device__ __forceinline__ int swz16(int row, int at) { return at ^ (row & 15); 
 __device__ __forceinline__ float silu(float g) {
   constexpr float kLog2e = 1.44269504f, kLog2eLo = 1.9259630e-8f, kLn2 = 0.693147181f;
   const float hi = -g * kLog2e;
-  float lo = fmaf(-g, kLog2eLo, fmaf(-g, kLog2e, -hi));
-  lo = fabsf(hi) < 126.0f ? lo : 0.0f;   // past that 2^hi is 0 or infinite, or g is no number
-  const float x = __builtin_amdgcn_exp2f(hi);
-  return g * __builtin_amdgcn_rcpf(1.0f + fmaf(x, lo * kLn2, x));
+  const float lo = fmaf(-g, kLog2eLo, fmaf(-g, kLog2e, -hi));
+  float x = __builtin_amdgcn_exp2f(hi);
+  // past that 2^hi is or nears 0 or infinity (whose product with lo is no number)
+  x = fabsf(hi) < 126.0f ? fmaf(x, lo * kLn2, x) : x;
+  return g * __builtin_amdgcn_rcpf(1.0f + x);
 }
 
 template <typename OutT, int C>
