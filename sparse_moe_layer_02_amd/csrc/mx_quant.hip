@@ -6,7 +6,7 @@
 // bits without sign, which ranks infinities and NaNs above every number and
 // carries the exponent in place: scale byte = max(exponent field - 2, 0).
 // Values are read and written past the caches (each is touched once): 65168 x
-// 2048 bf16 values to codes and back to fp32, 0.94 GB, in 186 us before, 150
+// 2048 bf16 values to codes and back to fp32, 0.94 GB, in 186 us before, 145
 // with it; codes and scales keep the default policy, the product that follows
 // reads them.
 #include "block_internal.h"
