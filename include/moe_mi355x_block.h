@@ -64,7 +64,8 @@ moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int
  * out [rows_cap][N] (swiglu: [rows_cap][N / 2]) in out_dtype.
  * MOE_ERR_SHAPE: rows_cap < 1, n_experts outside 0..4096, D < 1 or D % 128,
  *   N < 1 or N % 16, N * D >= 2^31, T < 1, K < 1 or T*K >= 2^31 with row_src,
- *   or more blocks than a launch takes.
+ *   more than 2^39 values in the rows of a (T * D with row_src, rows_cap * D
+ *   without), or more blocks than a launch takes.
  * MOE_ERR_ALIGN: a, w, out 16 bytes; a_scales, w_scales, offsets, row_src 4;
  *   ws 256.  n_experts == 0 enqueues nothing (w, w_scales may be NULL).
  * ws: at least moe_grouped_gemm_mxfp4_workspace_bytes(rows_cap, n_experts). */
@@ -85,7 +86,8 @@ moe_status moe_grouped_gemm_mxfp4(const void *a, const uint8_t *a_scales, const 
  * by moe_mxfp4_quantize (y_perm is bitwise that of the three calls).
  * y_perm [rows_cap][H] bf16; rows past offsets[n_ffn] are left as they were.
  * T, K, row_src, offsets, rows_cap as for moe_expert_ffn_gather.
- * MOE_ERR_SHAPE also for H % 128 or I % 128 and for 2 * I * H >= 2^31.
+ * MOE_ERR_SHAPE also for H % 128 or I % 128, for 2 * I * H >= 2^31 and for
+ * T * H or rows_cap * I past 2^39.
  * ws: at least moe_expert_ffn_mxfp4_workspace_bytes(rows_cap, n_ffn, I). */
 size_t moe_expert_ffn_mxfp4_workspace_bytes(int rows_cap, int n_ffn, int I);
 moe_status moe_expert_ffn_mxfp4(const void *x, const uint8_t *x_scales, int T, int K,

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kMaxExperts = 4096;
 constexpr int kMaxNorm = 32768;
+constexpr long long kMaxRowValues = 1ll << 39;   // a row's address is 32 bits of 128 values
 
 inline bool dtype_ok(int d) { return d == MOE_F32 || d == MOE_BF16; }
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -35,6 +36,7 @@ moe_status product_sizes(const int32_t* row_src, int T, int K, int rows_cap, int
       N % 16 || !fits_i32((long long)N * D) || !mx::grid_fits(rows_cap, n_experts, N))
     return MOE_ERR_SHAPE;
   if (row_src && (T < 1 || K < 1 || !fits_i32((long long)T * K))) return MOE_ERR_SHAPE;
+  if ((long long)(row_src ? T : rows_cap) * D > kMaxRowValues) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 

@@ -327,10 +327,13 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
 #pragma unroll
     for (int i = 0; i < NQ; ++i) src[i] = min(max(src[i], 0) / p.K, p.T - 1);
   }
-  uint32_t arow[R];                              // in 16-byte units from a
+  // A row's address in 32 bits: in units of 128 values, which a row is a whole
+  // number of (2^39 values at most, the host checks)
+  constexpr int kUnit = A4 ? 6 : 8;              // log2 of a unit's bytes
+  uint32_t arow[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) arow[i] = (uint32_t)(((size_t)src[i] * a_pitch) >> 4);
-  auto row_ptr = [&](int i) { return (const char*)p.a + ((size_t)arow[i] << 4); };
+  for (int i = 0; i < R; ++i) arow[i] = (uint32_t)(((size_t)src[i] * a_pitch) >> kUnit);
+  auto row_ptr = [&](int i) { return (const char*)p.a + ((size_t)arow[i] << kUnit); };
 
   typename M::Acc acc[RB][NB];
 #pragma unroll
