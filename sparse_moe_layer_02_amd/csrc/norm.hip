@@ -9,12 +9,15 @@
 // sums still in registers, so a row costs its inputs and outputs and no more.
 // A row of at most 512 P values is one wave's and needs no barrier, four such
 // rows to a block; longer ones are a block's.
+#include <algorithm>
+
 #include "block_internal.h"
 
 namespace moe {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr unsigned kMaxGridX = 1u << 21;   // blocks of at most kMaxThreads
 
 template <typename T> struct Row8;
 template <> struct Row8<bf16> {
@@ -59,14 +62,19 @@ __device__ __forceinline__ float row_sum(float v, float* part, bool one_wave) {
   return v;
 }
 
+// The row of a thread.  The grid is a rectangle of blocks in row order.
+__device__ __forceinline__ unsigned row_of_thread() {
+  return (blockIdx.y * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
+}
+
 // blockDim (threads of a row, rows of a block); one_wave: 64 threads a row.
 template <typename T, typename U, int P>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const T* x, const float* __restrict__ w,
                                                            float eps, int rows, int H, U* y) {
   __shared__ float part[kMaxThreads / kWave];
   const bool one_wave = blockDim.x == kWave;
-  const int t = blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= rows) return;   // a whole wave, and then blocks have no barrier
+  const unsigned t = row_of_thread();
+  if (t >= (unsigned)rows) return;   // a whole wave, and then blocks have no barrier
   float v[P][8];
   float ss = 0.0f;
 #pragma unroll
@@ -99,8 +107,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_residual_kernel(
     Y* next, int rows, int H) {
   __shared__ float part[2][kMaxThreads / kWave];
   const bool one_wave = blockDim.x == kWave;
-  const int t = blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= rows) return;
+  const unsigned t = row_of_thread();
+  if (t >= (unsigned)rows) return;
   float v[P][8], s[P][8];
   float ss = 0.0f;
 #pragma unroll
@@ -168,7 +176,10 @@ Shape shape(int T, int H) {
   const int per = ((H + 8 * s.P - 1) / (8 * s.P) + kWave - 1) / kWave * kWave;
   const int rows = per == kWave ? 4 : 1;
   s.block = dim3(per, rows);
-  s.grid = dim3(ceil_div(T, rows));
+  // a launch takes fewer than 2^32 threads along a dimension of its grid
+  const unsigned blocks = ceil_div(T, rows);
+  s.grid.x = std::min(blocks, kMaxGridX);
+  s.grid.y = ceil_div(blocks, s.grid.x);
   return s;
 }
 
