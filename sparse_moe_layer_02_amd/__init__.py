@@ -504,9 +504,17 @@ def forward(x, w_router, bias, w13, w2, K, ffn_scale, buf):
     w13 and w2 may be MXFP4 (quantize_weights), with bf16 tokens and buffers of
     alloc_buffers(..., mxfp4=True): the experts then run on 4-bit weights
     (moe_expert_ffn_mxfp4)."""
+    _same_form(w13, w2)
     if buf["y_acc"] is None:
         return _forward_fused(x, w_router, bias, w13, w2, K, ffn_scale, buf)
     return _forward_six(x, w_router, bias, w13, w2, K, ffn_scale, buf)
+
+
+def _same_form(w13, w2):
+    """Refuse expert weights of which one is MXFP4 and the other is not, before
+    the first call of a pass."""
+    if isinstance(w13, MXFP4) != isinstance(w2, MXFP4):
+        raise TypeError("w13 and w2: both MXFP4 or neither")
 
 
 def _forward_fused(x, w_router, bias, w13, w2, K, ffn_scale, buf):
@@ -573,6 +581,7 @@ def _dispatch_and_experts(x, K, n_ffn, w13, w2, buf):
 def forward_serial(x, w_router, bias, w13, w2, K, ffn_scale, buf):
     """forward() with every call on the current stream in layer order (the
     six-call path does not use its second stream)."""
+    _same_form(w13, w2)
     if buf["y_acc"] is None:
         return _forward_fused(x, w_router, bias, w13, w2, K, ffn_scale, buf)
     n_ffn = w13.shape[0]

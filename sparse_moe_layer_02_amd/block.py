@@ -51,8 +51,9 @@ GATES = {"none": 0, "channel": 1, "token": 2}
 
 class MXFP4(NamedTuple):
     """Rows of C values in microscaled 4-bit floating point: codes
-    [..., C / 2] and scales [..., C / 32], both uint8 (forward() and
-    moe_forward's siblings take it in the place of bf16 expert weights)."""
+    [..., C / 2] and scales [..., C / 32], both uint8.  forward(),
+    forward_serial() and block_forward() take a pair of them in the place of
+    bf16 expert weights."""
     codes: torch.Tensor
     scales: torch.Tensor
 
@@ -216,7 +217,8 @@ def block_forward(h, w_norm, w_router, bias, w13, w2, K, ffn_scale, buf, scale=1
     block's norm.  buf: alloc_buffers(..., residual=h.dtype).  Returns
     buf["h_out"], and with w_next also buf["h_norm"], the next block's input
     (it shares no buffer with this block's, buf["x_norm"])."""
-    from . import forward
+    from . import _same_form, forward
+    _same_form(w13, w2)
     moe_norm(h, w_norm, buf["x_norm"], eps)
     y = forward(buf["x_norm"], w_router, bias, w13, w2, K, ffn_scale, buf)
     n = buf["h_norm"] if w_next is not None else None
