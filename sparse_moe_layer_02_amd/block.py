@@ -45,6 +45,11 @@ def _call(name, device, *args):
             _check(name, f(*args, torch._C._cuda_getCurrentRawStream(i)))
 
 
+def _int(*sizes):
+    """Sizes that the C calls take as int: ctypes would drop their upper bits."""
+    _require(max(sizes) < 1 << 31, "sizes below 2^31")
+
+
 BLOCK = 32                     # values that share a scale
 GATES = {"none": 0, "channel": 1, "token": 2}
 
@@ -78,6 +83,7 @@ def moe_mxfp4_quantize(x, codes, scales, n_rows=None):
     d = _dev(x, codes, scales, n_rows)
     _require(_mx(codes, scales, "codes") == tuple(x.shape), "codes and scales of x's shape")
     cols = x.shape[-1]
+    _int(cols)
     if n_rows is not None:
         _want(n_rows, torch.int32, "n_rows")
         _require(n_rows.numel() >= 1, "n_rows.numel() >= 1")
@@ -90,6 +96,7 @@ def moe_mxfp4_dequantize(codes, scales, y):
     d = _dev(codes, scales, y)
     _require(_mx(codes, scales, "codes") == tuple(y.shape), "codes and scales of y's shape")
     cols = y.shape[-1]
+    _int(cols)
     _call("moe_mxfp4_dequantize", d, _p(codes), _p(scales), _DT[y.dtype],
           y.numel() // max(cols, 1), cols, _p(y))
 
@@ -120,6 +127,7 @@ def moe_grouped_gemm_mxfp4(a, a_scales, offsets, w, w_scales, out, ws, row_src=N
     _want(offsets, torch.int32, "offsets")
     E, N, D = _mx(w, w_scales, "w")
     rows_cap, width = out.shape
+    _int(a.shape[0], K, rows_cap, E, D, N)
     if a_scales is None:
         _want(a, torch.bfloat16, "a")
         _require(a.dim() == 2 and a.shape[1] == D, "a.shape[1] == D")
@@ -159,6 +167,7 @@ def moe_expert_ffn_mxfp4(x, x_scales, K, row_src, offsets, w13, w13_scales, w2, 
     else:
         _require(_mx(x, x_scales, "x")[1:] == (H,), "x of H values a row")
     rows_cap = y_perm.shape[0]
+    _int(x.shape[0], K, rows_cap, N, H, I2)
     _require(y_perm.shape == (rows_cap, H) and row_src.numel() >= rows_cap,
              "y_perm of H columns and row_src.numel() >= rows_cap")
     _require(offsets.numel() >= N + 1, "offsets.numel() >= n_ffn + 1")
@@ -178,6 +187,7 @@ def moe_norm(x, weight, y, eps=1e-5):
     None: ones)."""
     d = _dev(x, weight, y)
     T, H = x.shape
+    _int(T, H)
     _norm_weight(weight, H, "weight")
     _require(y.shape == (T, H), "y.shape == x.shape")
     _call("moe_norm", d, _p(x), _DT[x.dtype], _p(weight), eps, T, H, _p(y), _DT[y.dtype])
@@ -190,6 +200,7 @@ def moe_norm_residual(y, residual, out, scale=1.0, w_post=None, gate=None, gate_
     "none", "channel" (gate [H]) or "token" (gate [T])."""
     d = _dev(y, residual, out, w_post, gate, w_next, next_out)
     T, H = y.shape
+    _int(T, H)
     _norm_weight(w_post, H, "w_post")
     _norm_weight(w_next, H, "w_next")
     _require(gate_kind in GATES and (gate is None) == (gate_kind == "none"),

@@ -45,3 +45,63 @@ def test_one_expert_weight_in_mxfp4_and_the_other_not(recorded, forward, separat
     for w13, w2 in (plain, packed):
         f(x, w_router, bias, w13, w2, K, 1.0, buf)
     assert recorded.count("moe_expert_ffn_gather") == recorded.count("moe_expert_ffn_mxfp4") == 1
+
+
+@pytest.fixture
+def no_gpu(monkeypatch):
+    """The block's binding on tensors without memory; the library's calls are recorded."""
+    calls = []
+    monkeypatch.setattr(moe.block, "_dev", lambda *ts: torch.device("cuda", 0))
+    monkeypatch.setattr(moe.block, "_call", lambda name, *a: calls.append(name))
+    return calls
+
+
+def _meta(*shape, dtype=BF16):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def _meta_q(*shape):
+    return (_meta(*shape[:-1], shape[-1] // 2, dtype=U8), _meta(*shape[:-1], shape[-1] // 32, dtype=U8))
+
+
+BIG = 1 << 32                                        # 32 bits of it are 0
+
+
+def test_sizes_past_31_bits_are_refused(no_gpu):
+    """The C calls take int: a size that would lose its upper bits on the way is an error, not
+    another size.  At the sizes below the same calls go through."""
+    i32 = torch.int32
+    for T, H, ok in ((2 ** 31 - 1, 8, True), (BIG + 1, 8, False), (1, BIG + 8, False)):
+        x = _meta(T, H)
+        for f in (lambda: moe.moe_norm(x, None, x), lambda: moe.moe_norm_residual(x, x, x)):
+            _expect(f, ok, no_gpu)
+    for C, ok in ((2 ** 31 - 32, True), (BIG + 32, False)):
+        x, q = _meta(2, C), _meta_q(2, C)
+        _expect(lambda: moe.moe_mxfp4_quantize(x, *q), ok, no_gpu)
+        _expect(lambda: moe.moe_mxfp4_dequantize(*q, x), ok, no_gpu)
+    off, ws = _meta(3, dtype=i32), _meta(256, dtype=U8)
+    for rows, cap, D, N, K, ok in ((2 ** 31 - 1, 8, 128, 16, 1, True), (BIG + 9, 8, 128, 16, 1, False),
+                                   (BIG + 9, BIG + 8, 128, 16, 1, False),
+                                   (8, 8, BIG + 128, 16, 1, False), (8, 8, 128, BIG + 16, 1, False),
+                                   (8, 8, 128, 16, BIG + 1, False)):
+        w, out = _meta_q(2, N, D), _meta(cap, N)
+        for a in ((_meta(rows, D), None), _meta_q(rows, D)):
+            _expect(lambda: moe.moe_grouped_gemm_mxfp4(*a, off, *w, out, ws, K=K), ok, no_gpu)
+    for T, cap, H, I, K, ok in ((2 ** 31 - 1, 8, 128, 128, 1, True), (BIG + 1, 8, 128, 128, 1, False),
+                                (8, BIG + 8, 128, 128, 1, False), (8, 8, BIG + 128, 128, 1, False),
+                                (8, 8, 128, BIG + 128, 1, False), (8, 8, 128, 128, BIG + 1, False)):
+        w13, w2 = _meta_q(2, 2 * I, H), _meta_q(2, H, I)
+        src, y = _meta(cap, dtype=i32), _meta(cap, H)
+        _expect(lambda: moe.moe_expert_ffn_mxfp4(_meta(T, H), None, K, src, off, *w13, *w2, y, ws),
+                ok, no_gpu)
+
+
+def _expect(f, ok, calls):
+    calls.clear()
+    if ok:
+        f()
+        assert len(calls) == 1
+    else:
+        with pytest.raises(ValueError, match="2\\^31"):
+            f()
+        assert calls == []
