@@ -57,6 +57,14 @@ __device__ __forceinline__ void wave_lds_sync() {
   asm volatile("" ::: "memory");
 }
 
+// The same order for the compiler alone: it moves no memory access across this
+// point.  LDS serves a wave's accesses in the order in which they are issued,
+// so what another lane of the wave wrote before it is read without a wait.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 inline unsigned ceil_div(size_t a, size_t b) { return (unsigned)((a + b - 1) / b); }
 
 // ---- opt-in per-kernel event timing (profile.hip) --------------------------

@@ -254,8 +254,10 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   auto write_w = [&](auto B) {
     constexpr int b = decltype(B)::value;
     char* d = wlds + (lane >> 3) * 128 + ((lane & 7) ^ (lane >> 3)) * 16;
+    wave_lds_order();                            // behind the reads of the step before
 #pragma unroll
     for (int i = 0; i < NL; ++i) *(i32x4*)(d + i * 1024) = wr[b][i];
+    wave_lds_order();                            // in front of other lanes' reads
   };
   i32x4 fw[2][NB][U];                            // codes of a slice, by its parity
   auto read_w = [&](auto T) {                    // slice T of the step in LDS
@@ -297,10 +299,12 @@ __device__ __forceinline__ void tile(char* smem, const GemmArgs& p, int e, int r
   };
   int sw[NB][U];
   auto pass_scales = [&] {
+    wave_lds_order();
 #pragma unroll
     for (int i = 0; i < NS; ++i)
       if (16 * CB >= 64 || lane < 16 * CB)
         *(i32x4*)(slds + (lane + 64 * i) * 16) = scale_dwords(wsr[i]);
+    wave_lds_order();
 #pragma unroll
     for (int b = 0; b < NB; ++b) read_scales(slds + (MS * b + m) * 16, sw[b]);
   };
