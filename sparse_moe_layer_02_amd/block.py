@@ -221,17 +221,27 @@ def moe_norm_residual(y, residual, out, scale=1.0, w_post=None, gate=None, gate_
 
 
 def block_forward(h, w_norm, w_router, bias, w13, w2, K, ffn_scale, buf, scale=1.0, w_post=None,
-                  gate=None, gate_kind="none", w_next=None, eps=1e-5):
+                  gate=None, gate_kind="none", w_next=None, eps=1e-5, x_norm=None):
     """The MoE layer as a block of a residual stream h [T, H] (fp32 or bf16),
     on the current stream: norm, layer (forward(), with bf16 or MXFP4 expert
     weights), norm of its output, gate, residual scale and sum, and the next
     block's norm.  buf: alloc_buffers(..., residual=h.dtype).  Returns
-    buf["h_out"], and with w_next also buf["h_norm"], the next block's input
-    (it shares no buffer with this block's, buf["x_norm"])."""
+    buf["h_out"], and with w_next also buf["h_norm"]: the layer's input of a
+    block that follows, which takes it as its x_norm.
+    x_norm: the norm of h, where there is one already ([T, H] in the layer's
+    dtype, its weight applied); the norm in front is then left out, and w_norm
+    has to be None.  In a chain of blocks h and x_norm may be the last block's
+    results in the same buf: they are read before this block's are written."""
     from . import _same_form, forward
     _same_form(w13, w2)
-    moe_norm(h, w_norm, buf["x_norm"], eps)
-    y = forward(buf["x_norm"], w_router, bias, w13, w2, K, ffn_scale, buf)
+    if x_norm is None:
+        x_norm = buf["x_norm"]
+        moe_norm(h, w_norm, x_norm, eps)
+    else:
+        _require(w_norm is None, "w_norm None with x_norm")
+        _require(x_norm.shape == h.shape and x_norm.dtype == buf["y"].dtype,
+                 "x_norm of h's shape in the layer's dtype")
+    y = forward(x_norm, w_router, bias, w13, w2, K, ffn_scale, buf)
     n = buf["h_norm"] if w_next is not None else None
     moe_norm_residual(y, h, buf["h_out"], scale, w_post, gate, gate_kind, w_next, n, eps)
     return buf["h_out"] if n is None else (buf["h_out"], n)

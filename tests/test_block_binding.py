@@ -105,3 +105,19 @@ def _expect(f, ok, calls):
         with pytest.raises(ValueError, match="2\\^31"):
             f()
         assert calls == []
+
+
+def test_block_takes_a_norm_that_is_there_already(recorded):
+    x, w_router, bias, _, (w13, w2), K, buf = _layer()
+    buf.update(x_norm=x.clone(), h_norm=x.clone(), h_out=x.clone(), y=x.clone())
+    run = lambda w_norm, **k: moe.block_forward(x, w_norm, w_router, bias, w13, w2, K, 1.0, buf, **k)  # noqa: E731
+    run(None)
+    assert recorded[0] == "moe_norm" and recorded.count("moe_norm") == 1
+    recorded.clear()
+    run(None, x_norm=buf["h_norm"])
+    assert "moe_norm" not in recorded and recorded[-1] == "moe_norm_residual"
+    recorded.clear()
+    for w_norm, x_norm in ((torch.ones(128), buf["h_norm"]), (None, x[:4]), (None, x.float())):
+        with pytest.raises(ValueError, match="x_norm"):
+            run(w_norm, x_norm=x_norm)
+    assert recorded == []
