@@ -100,7 +100,9 @@ moe_status moe_expert_ffn_mxfp4(const void *x, const uint8_t *x_scales, int T, i
 /* The norm before a block (root mean square):
  *   y[t] = x[t] / sqrt(mean over h of x[t][h]^2 + eps) * weight[h]
  * x [T][H] in x_dtype, weight [H] fp32 or NULL (ones), y [T][H] in y_dtype;
- * fp32 arithmetic.  y may be x when the dtypes are equal.
+ * fp32 arithmetic; rows whose squares fp32 cannot hold are scaled by a power of
+ * two first, so that finite rows of any size are normed.  y may be x when the
+ * dtypes are equal.
  * MOE_ERR_SHAPE: T < 1, H < 1, H % 8, H > 32768, or eps negative or not
  * finite.  MOE_ERR_ALIGN: x, y, weight 16 bytes. */
 moe_status moe_norm(const void *x, int x_dtype, const float *weight, float eps, int T, int H,

@@ -62,6 +62,36 @@ __device__ __forceinline__ float row_sum(float v, float* part, bool one_wave) {
   return v;
 }
 
+// 1 / sqrt(mean(v^2) + eps) of a row whose threads hold the sums ss of their
+// v's squares.  Squares past 2^128 leave no sum, and below 2^-126 they lose
+// digits (which counts where eps does not cover them): such a row's v, rare and
+// the same for all its threads, are scaled by a power of two, eps by its
+// square, and summed again.  The scaled v times the root is the norm as before.
+// part: two sums' LDS.
+template <int P>
+__device__ __forceinline__ float inv_rms(float (&v)[P][8], float ss, float eps, int H,
+                                         float (*part)[kMaxThreads / kWave], bool one_wave) {
+  float sum = row_sum(ss, part[0], one_wave);
+  const bool large = !(sum < __builtin_inff()), small = sum < 0x1p-90f && eps < 0x1p-100f;
+  if (large || small) {
+    const float f = large ? 0x1p-96f : 0x1p96f;
+    ss = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if ((p * (int)blockDim.x + (int)threadIdx.x) * 8 < H) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[p][i] *= f;
+          ss = fmaf(v[p][i], v[p][i], ss);
+        }
+      }
+    }
+    sum = row_sum(ss, part[1], one_wave);
+    eps = eps * f * f;
+  }
+  return rsqrtf(sum / (float)H + eps);
+}
+
 // The row of a thread.  The grid is a rectangle of blocks in row order.
 __device__ __forceinline__ unsigned row_of_thread() {
   return (blockIdx.y * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
@@ -71,7 +101,7 @@ __device__ __forceinline__ unsigned row_of_thread() {
 template <typename T, typename U, int P>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const T* x, const float* __restrict__ w,
                                                            float eps, int rows, int H, U* y) {
-  __shared__ float part[kMaxThreads / kWave];
+  __shared__ float part[2][kMaxThreads / kWave];
   const bool one_wave = blockDim.x == kWave;
   const unsigned t = row_of_thread();
   if (t >= (unsigned)rows) return;   // a whole wave, and then blocks have no barrier
@@ -86,7 +116,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(const T* x, const flo
       for (int i = 0; i < 8; ++i) ss = fmaf(v[p][i], v[p][i], ss);
     }
   }
-  const float r = rsqrtf(row_sum(ss, part, one_wave) / (float)H + eps);
+  const float r = inv_rms(v, ss, eps, H, part, one_wave);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int h = (p * blockDim.x + threadIdx.x) * 8;
@@ -105,7 +135,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_residual_kernel(
     const Y* y, const float* __restrict__ w_post, float eps, const float* __restrict__ gate,
     int gate_kind, float scale, const S* residual, S* res_out, const float* __restrict__ w_next,
     Y* next, int rows, int H) {
-  __shared__ float part[2][kMaxThreads / kWave];
+  __shared__ float part[4][kMaxThreads / kWave];
   const bool one_wave = blockDim.x == kWave;
   const unsigned t = row_of_thread();
   if (t >= (unsigned)rows) return;
@@ -123,7 +153,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_residual_kernel(
   }
   float r = scale;
   if (gate_kind == MOE_GATE_TOKEN) r *= gate[t];
-  if (w_post) r *= rsqrtf(row_sum(ss, part[0], one_wave) / (float)H + eps);
+  if (w_post) r *= inv_rms(v, ss, eps, H, part, one_wave);
   ss = 0.0f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -149,7 +179,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_residual_kernel(
     }
   }
   if (!next) return;
-  r = rsqrtf(row_sum(ss, part[1], one_wave) / (float)H + eps);
+  r = inv_rms(s, ss, eps, H, part + 2, one_wave);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int h = (p * blockDim.x + threadIdx.x) * 8;
