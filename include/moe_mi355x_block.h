@@ -41,8 +41,10 @@ moe_status moe_mxfp4_quantize(const void *x, int dtype, long long rows, int cols
                               const int32_t *n_rows, uint8_t *codes, uint8_t *scales,
                               void *stream);
 
-/* The values that MXFP4 rows stand for, in dtype (every finite one is exact
- * in fp32 and in bf16; 4 * 2^127 and 6 * 2^127 become infinities).
+/* The values that MXFP4 rows stand for, in dtype: exact in fp32 and in bf16,
+ * but for magnitudes of 2^128 and more, which become infinities (4 and 6 at
+ * scale byte 253, 2 to 6 at 254; moe_mxfp4_quantize writes no scale byte over
+ * 252 but 255).
  * y [rows][cols] (16-byte aligned); the rest as for moe_mxfp4_quantize. */
 moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int dtype,
                                 long long rows, int cols, void *y, void *stream);
@@ -52,8 +54,10 @@ moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int
  *   c[n] = sum over d of a(r)[d] * w[e][n][d],  n < N, fp32 accumulation
  *   out[r] = c, or with swiglu silu(c[j]) * c[N / 2 + j] for j < N / 2
  * a: the rows, in one of two forms:
- *   a_scales NULL: bf16 [.][D];
- *   else MXFP4: codes [.][D / 2] in a, scales [.][D / 32] in a_scales.
+ *   a_scales NULL: bf16 [.][D].  The weights count as bf16 values too, those
+ *     of 2^128 and more as infinities (as in moe_mxfp4_dequantize);
+ *   else MXFP4: codes [.][D / 2] in a, scales [.][D / 32] in a_scales.  Every
+ *     product is that of the values themselves.
  * row_src: NULL, and a(r) = a[r] with rows_cap rows in a; or the dispatch
  *   indices of moe_permute (capacity rows_cap), and a(r) = a[row_src[r] / K]
  *   with T rows in a (indices outside [0, T*K) are clamped to a row of a).

@@ -175,6 +175,36 @@ def test_experts_on_4bit_rows_are_their_three_calls_in_either_kernel():
     assert torch.equal(y[:S], z[:S]) and torch.isfinite(y[:S].float()).all()
 
 
+# ------------------------------------------------------- the largest scales --
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("byte", [0, 1, 251, 252, 253, 254])
+@pytest.mark.parametrize("cap", [4, 200])
+def test_weights_at_the_least_and_largest_scales(kind, byte, cap):
+    """Every code at the ends of the scales: 4-bit rows multiply the values themselves, bf16 rows the
+    values in bf16, where 2^128 and more is an infinity.  Powers of two in the rows: nothing rounds."""
+    D, N = 128, 16
+    c = np.zeros((1, N, D // 2), np.uint8)
+    c[0, :, 0] = np.arange(16)                       # value 0 of weight row n is code n, the rest 0
+    s = np.full((1, N, D // 32), byte, np.uint8)
+    a = np.zeros((4, D))
+    a[:, 0] = [2.0 ** -100, 2.0 ** -3, 0.0, -(2.0 ** -120)]
+    a[2, 1] = 1.0
+    qa, qs = quantize(a)
+    t, ts = (_dev(a, BF16), None) if kind == "bf16" else (_dev(qa), _dev(qs))
+    pad = lambda x: None if x is None else torch.cat([x, x[:1].expand(cap - 4, -1)]).contiguous()  # noqa: E731
+    y = torch.empty((cap, N), dtype=F32, device=device())
+    moe.moe_grouped_gemm_mxfp4(pad(t), pad(ts), _dev(spans([cap])), _dev(c), _dev(s), y, _work(cap, 1))
+    w = values(c[0], s[0])
+    with np.errstate(over="ignore", invalid="ignore"):
+        if kind == "bf16":
+            w = np.where(np.abs(w) >= 2.0 ** 128, np.sign(w) * np.inf, w)
+        want = (a[:, None, :2] * w[None, :, :2]).sum(-1).astype(np.float32)
+    got, tiny = host(y)[:4], np.abs(want) < 2.0 ** -126
+    same = (got == want) | (np.isnan(got) & np.isnan(want)) | (tiny & (np.abs(got) <= 2.0 ** -126))
+    assert same.all(), (got[~same], want[~same])
+
+
 # ------------------------------------------------------- malformed offsets --
 
 LO, HI = -(1 << 31), (1 << 31) - 1
