@@ -72,7 +72,11 @@ moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int
  *   without), or more blocks than a launch takes.
  * MOE_ERR_ALIGN: a, w, out 16 bytes; a_scales, w_scales, offsets, row_src 4;
  *   ws 256.  n_experts == 0 enqueues nothing (w, w_scales may be NULL).
- * ws: at least moe_grouped_gemm_mxfp4_workspace_bytes(rows_cap, n_experts). */
+ * ws: at least moe_grouped_gemm_mxfp4_workspace_bytes(rows_cap, n_experts).
+ * The kernel is chosen by the sizes alone: the one for small batches with at
+ * most 16 rows an expert (rows_cap, or with row_src T, at most 16), or with at
+ * most 128 and rows_cap <= 8 * n_experts.  A batch of few rows runs faster in a
+ * buffer within that. */
 size_t moe_grouped_gemm_mxfp4_workspace_bytes(int rows_cap, int n_experts);
 moe_status moe_grouped_gemm_mxfp4(const void *a, const uint8_t *a_scales, const int32_t *row_src,
                                   int T, int K, const int32_t *offsets, int rows_cap,
@@ -124,8 +128,9 @@ moe_status moe_norm(const void *x, int x_dtype, const float *weight, float eps, 
  * y [T][H] in y_dtype, residual and res_out [T][H] in res_dtype.  res_out may
  * be residual, and next may be y; no other two may overlap.
  * A scale or gate of zero adds zero times z (a NaN in z stays one).
- * Errors as for moe_norm, MOE_ERR_SHAPE also for a scale that is not finite
- * or an unknown gate kind, MOE_ERR_NULL for a gate kind without a gate. */
+ * Errors as for moe_norm (every pointer 16-byte aligned, a token gate too),
+ * MOE_ERR_SHAPE also for a scale that is not finite or an unknown gate kind,
+ * MOE_ERR_NULL for a gate kind without a gate. */
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
 moe_status moe_norm_residual(const void *y, int y_dtype, const float *w_post, float eps,
                              const float *gate, int gate_kind, float scale, const void *residual,

@@ -146,6 +146,11 @@ moe_status moe_expert_ffn_mxfp4(const void* x, const uint8_t* x_scales, int T, i
   const hipStream_t s = (hipStream_t)stream;
   const int most = rows_max(row_src, rows_cap, T);
   hipError_t e = mx::launch_tiles(offsets, rows_cap, n_ffn, most, x_scales != nullptr, f.list, s);
+  // hh is rounded to bf16, as between the products of moe_expert_ffn: the matrix
+  // cores multiply bf16 rows, and its remaining digits as rows of their own would
+  // take twice the instructions in the down product.  It costs as much as the
+  // output's own rounding: outputs are 0.0023 of their norm from the 64-bit form,
+  // of which either rounding alone makes 0.0017.
   if (e == hipSuccess)
     e = mx::launch_product(x, x_scales, row_src, T, K, offsets, rows_cap, n_ffn, most, H, 2 * I,
                            w13, w13_scales, true, MOE_BF16, f.hh, f.list, s);

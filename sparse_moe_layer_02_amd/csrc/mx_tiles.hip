@@ -14,9 +14,14 @@ constexpr size_t kHeader = 256;
 inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 // m-tiles of bm rows at most; workspaces hold the list of either form of rows
 inline int tile_rows(bool fp4_rows) { return fp4_rows ? kMaxRows<true> : kMaxRows<false>; }
-// Whether the experts have few rows each: no expert more than 16, or on average
-// at most 8 and none over 128 (one that does have many is read once for every
-// 16 rows, which costs less than the list, about 10 us a call).
+// Whether the experts have few rows each, as far as the host can tell, which
+// sees the buffer and not the rows in it: no expert more than 16, or at most 8
+// rows of the buffer an expert and none over 128.  An expert that does have
+// many is read past the caches once for every 16 rows.  Experts of 6144 x 2048,
+// 45 of 64 with one row and one with m, in microseconds, this way against the
+// list: m = 1: 166, 193; 16: 160, 193; 32: 179, 193; 64: 219, 207; 128: 327,
+// 237.  The same batch (64 tokens, K 12, 64 of 768 experts) takes 162-170 in a
+// buffer of 120 rows and 191-195 in one of 768, which is over 8 an expert.
 inline bool few_rows(int rows_cap, int n_experts, int rows_max) {
   return rows_max <= kFewRows || (rows_max <= 128 && (long long)rows_cap <= 8ll * n_experts);
 }

@@ -7,7 +7,7 @@
 // pieces, P of them a thread), its sum of squares is taken in fp32 (a fixed
 // order: bitwise the same from run to run), and the second norm works on the
 // sums still in registers, so a row costs its inputs and outputs and no more.
-// A row of at most 512 P values is one wave's and needs no barrier, four such
+// A row of at most 512 values is one wave's and needs no barrier, four such
 // rows to a block; longer ones are a block's.
 #include <algorithm>
 
@@ -198,8 +198,8 @@ struct Shape {
   dim3 block, grid;
 };
 // Rows of up to 2048 values take one piece a thread, up to 16384 two, up to
-// 32768 four.  (8192 rows of 6144, residual in fp32: 111 us, 5.4 TB/s, with two
-// pieces, 114.5 us with one.)
+// 32768 four.  (8192 rows of 6144, residual in fp32: 113.5 us, 5.3 TB/s, with
+// two pieces; with one 3 % more.)
 Shape shape(int T, int H) {
   Shape s;
   s.P = H <= 2048 ? 1 : H <= 16 * kMaxThreads ? 2 : 4;
