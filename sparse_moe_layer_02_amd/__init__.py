@@ -72,7 +72,8 @@ def lib():
                 raise RuntimeError(f"{LIB_PATH} is missing: build it first "
                                    "(python -c 'import __graft_entry__ as g; g.build()')")
             l = ctypes.CDLL(LIB_PATH)
-            for name, (args, res) in (*_SIGS.items(), *_block.SIGS.items()):
+            for name, (args, res) in (*_SIGS.items(), *_block.SIGS.items(),
+                                      *_train.SIGS.items()):
                 f = getattr(l, name)
                 f.argtypes = args
                 f.restype = res
@@ -441,6 +442,15 @@ from .block import (MXFP4, block_forward, moe_expert_ffn_mxfp4,  # noqa: E402,F4
                     moe_expert_ffn_mxfp4_workspace_bytes, moe_grouped_gemm_mxfp4,
                     moe_grouped_gemm_mxfp4_workspace_bytes, moe_mxfp4_dequantize,
                     moe_mxfp4_quantize, moe_norm, moe_norm_residual, quantize_weights)
+
+# ------------- routing losses, backward passes of the norms, 8-bit activations --
+
+from . import train as _train  # noqa: E402
+from .train import (MXFP8, alloc_checkpoint, moe_balance_loss,  # noqa: E402,F401
+                    moe_balance_loss_workspace_bytes, moe_layer_norm, moe_layer_norm_backward,
+                    moe_mxfp8_dequantize, moe_mxfp8_quantize, moe_norm_backward,
+                    moe_norm_backward_workspace_bytes, moe_norm_checkpoint, moe_route_backward,
+                    moe_swiglu, moe_swiglu_backward)
 
 
 # ------------------------------------------------------- buffers + forward --

@@ -1,0 +1,209 @@
+"""The routing losses, their counts and the gradient of the router's logits against their 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+import _train as ref
+import sparse_moe_layer_02_amd as moe
+from _parity import device
+
+pytestmark = pytest.mark.gpu
+F32, I32 = torch.float32, torch.int32
+
+
+def _t(a, dtype=F32):
+    return torch.as_tensor(np.ascontiguousarray(a)).to(device()).to(dtype)
+
+
+def _case(T, E, K, n_seq, seed=0, masked=0.0, order="blocks"):
+    rng = np.random.default_rng(seed + T + E)
+    logits = (rng.standard_normal((T, E)) * 2 + rng.standard_normal(E)).astype(np.float32)
+    if masked:
+        logits[rng.random((T, E)) < masked] = -np.inf
+    key = np.where(np.isfinite(logits), logits, -1e9) + rng.standard_normal((T, E)) * 0.1
+    idx = np.argsort(-key, 1)[:, :K].astype(np.int32)
+    seq = None
+    if n_seq > 1:
+        seq = np.arange(T) * n_seq // T if order == "blocks" else rng.integers(0, n_seq, T)
+        seq = np.where(rng.random(T) < 0.2, rng.choice([-1, -5, n_seq, 1 << 30], T), seq).astype(np.int32)
+    return logits, idx, seq
+
+
+def _loss(logits, idx, seq, n_seq, group=None, bc=0.02, zc=0.003):
+    T, E = logits.shape
+    nan = lambda *s: torch.full(s, float("nan"), device=device())                       # noqa: E731
+    junk = lambda *s: torch.full(s, -77, dtype=I32, device=device())                    # noqa: E731
+    out = dict(counts=junk(n_seq, E), tokens=junk(n_seq + 1), load=nan(n_seq, E), losses=nan(2))
+    ws = torch.full((moe.moe_balance_loss_workspace_bytes(T, E, n_seq) + 64,), 255, dtype=torch.uint8,
+                    device=device())
+    moe.moe_balance_loss(logits, idx, ws=ws[:-64], seq=seq, group=group, balance_coef=bc, z_coef=zc, **out)
+    assert (ws[-64:] == 255).all()
+    return out
+
+
+def _check_loss(logits, idx, seq, n_seq, group=None, bc=0.02, zc=0.003):
+    got = _loss(_t(logits), _t(idx, I32), None if seq is None else _t(seq, I32), n_seq,
+                None if group is None else _t(group, I32), bc, zc)
+    want, e, counts, tokens, load = ref.balance_loss(logits.astype(np.float64), idx, seq, n_seq, group, bc, zc)
+    assert np.array_equal(got["counts"].cpu().numpy(), counts)
+    assert np.array_equal(got["tokens"].cpu().numpy(), tokens)
+    ref.close(got["load"], load, 2 * ref.U * load + 1e-37, "load")
+    ref.close(got["losses"], want, e + 1e-37, "losses")
+    return got
+
+
+SHAPES = [(1, 1, 1, 1), (1, 24, 4, 1), (3, 64, 64, 2), (5, 7, 3, 5), (70, 65, 2, 3), (257, 96, 8, 4),
+          (513, 130, 6, 1), (700, 257, 12, 9), (1031, 768, 12, 2), (300, 1000, 70, 3), (130, 1024, 5, 130)]
+
+
+@pytest.mark.parametrize("T,E,K,n_seq", SHAPES)
+@pytest.mark.parametrize("order", ["blocks", "mixed"])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_balance_loss(T, E, K, n_seq, order, grouped):
+    print(f"\n[case] balance T={T} E={E} K={K} n_seq={n_seq} {order} grouped={grouped}", flush=True)
+    logits, idx, seq = _case(T, E, K, n_seq, order=order)
+    group = None
+    if grouped:   # groups of all sizes, and experts left out
+        group = np.random.default_rng(E).integers(-1, max(1, E // 3) + 1, E).astype(np.int32)
+        group[0] = 0
+    _check_loss(logits, idx, seq, n_seq, group)
+
+
+@pytest.mark.parametrize("T,E,K,n_seq", [s for s in SHAPES if s[1] < 1000])
+@pytest.mark.parametrize("what", ["gates", "losses", "both"])
+def test_route_backward(T, E, K, n_seq, what):
+    print(f"\n[case] route_backward T={T} E={E} K={K} n_seq={n_seq} {what}", flush=True)
+    logits, idx, seq = _case(T, E, K, n_seq, masked=0.2)
+    rng = np.random.default_rng(T)
+    d_gate = rng.standard_normal((T, K)).astype(np.float32)
+    dl = np.array([700.0, -3.0], np.float32)
+    kw, rkw = {}, {}
+    if what != "gates":
+        _, _, _, tokens, load = ref.balance_loss(logits.astype(np.float64), idx, seq, n_seq)
+        load = load.astype(np.float32)
+        kw.update(tokens=_t(tokens, I32), load=_t(load), seq=None if seq is None else _t(seq, I32),
+                  d_losses=_t(dl), balance_coef=0.02, z_coef=0.003)
+        rkw.update(tokens=tokens, load=load.astype(np.float64), seq=seq, n_seq=n_seq, dl=dl.astype(np.float64),
+                   bc=float(np.float32(0.02)), zc=float(np.float32(0.003)))
+    if what != "losses":
+        kw.update(topk_idx=_t(idx, I32), d_gate=_t(d_gate))
+        rkw.update(idx=idx, d_gate=d_gate.astype(np.float64))
+    x = _t(logits)
+    d = torch.full_like(x, float("nan"))
+    moe.moe_route_backward(x, d, **kw)
+    want, e = ref.route_backward(logits.astype(np.float64), **rkw)
+    ref.close(d, want, e + 1e-37)
+    moe.moe_route_backward(x, x, **kw)               # in place: the same bits
+    assert torch.equal(x, d)
+
+
+def test_wide_pools_and_many_picks():
+    """1000 and 1024 experts, more picks than a wave has lanes."""
+    for T, E, K in ((9, 1000, 70), (5, 1024, 1024)):
+        logits, idx, _ = _case(T, E, K, 1)
+        d_gate = np.random.default_rng(1).standard_normal((T, K)).astype(np.float32)
+        d = torch.empty((T, E), device=device())
+        moe.moe_route_backward(_t(logits), d, _t(idx, I32), _t(d_gate))
+        want, e = ref.route_backward(logits.astype(np.float64), idx, d_gate.astype(np.float64))
+        ref.close(d, want, e + 1e-37)
+
+
+def test_picks_that_are_none_and_equal_picks():
+    logits, idx, seq = _case(40, 30, 6, 3)
+    idx[:, 1] = idx[:, 0]                            # twice the same expert
+    idx[:10, 2] = -1
+    idx[10:20, 3] = 30
+    idx[20:25, 4] = np.iinfo(np.int32).min
+    _check_loss(logits, idx, seq, 3)
+    d_gate = np.random.default_rng(1).standard_normal((40, 6)).astype(np.float32)
+    x, d = _t(logits), torch.empty((40, 30), device=device())
+    moe.moe_route_backward(x, d, _t(idx, I32), _t(d_gate))
+    want, e = ref.route_backward(logits.astype(np.float64), idx, d_gate.astype(np.float64))
+    ref.close(d, want, e + 1e-37)
+    again = torch.empty_like(d)
+    for _ in range(3):
+        moe.moe_route_backward(x, again, _t(idx, I32), _t(d_gate))
+        assert torch.equal(again, d)
+
+
+def test_rows_that_are_masked_and_padding_that_is_not_a_number():
+    """A token of -inf alone has no probabilities but counts as a token; NaN logits and gradients of
+    padding stay there; a pick of a masked expert may have any gradient."""
+    T, E, K, n = 24, 40, 4, 2
+    logits, idx, _ = _case(T, E, K, 1)
+    seq = (np.arange(T) * n // T).astype(np.int32)
+    logits[3] = -np.inf
+    logits[5, :] = -np.inf
+    logits[5, 7] = 2.5                               # one expert left
+    logits[8, :] = np.finfo(np.float32).min          # the lowest value is no mask where all have it
+    seq[8] = -1
+    seq[10:12] = -1
+    want = ref.balance_loss(logits.astype(np.float64), idx, seq, n, None, 0.02, 0.003)
+    bad = logits.copy()
+    bad[10], bad[11, 4] = np.nan, np.inf             # padding
+    got = _loss(_t(bad), _t(idx, I32), _t(seq, I32), n)
+    assert np.array_equal(got["tokens"].cpu().numpy(), want[3])
+    ref.close(got["losses"], want[0], want[1])
+    d_gate = np.random.default_rng(1).standard_normal((T, K)).astype(np.float32)
+    dirty = d_gate.copy()
+    dirty[3] = np.nan                                # every pick of token 3 is masked
+    dirty[5][idx[5] != 7] = np.inf
+    d = torch.full((T, E), float("nan"), device=device())
+    kw = dict(tokens=got["tokens"], load=got["load"], seq=_t(seq, I32), balance_coef=0.02, z_coef=0.003)
+    moe.moe_route_backward(_t(logits), d, _t(idx, I32), _t(dirty), **kw)
+    w, e = ref.route_backward(logits.astype(np.float64), idx, d_gate.astype(np.float64), seq, n, want[3],
+                              ref.f64(got["load"]), None, float(np.float32(0.02)), float(np.float32(0.003)))
+    ref.close(d, w, e + 1e-37)
+    assert (d[3] == 0).all()
+    moe.moe_route_backward(_t(bad), d, _t(idx, I32), _t(d_gate), **kw)      # rows of padding by themselves
+    rest = np.setdiff1d(np.arange(T), (10, 11))
+    w, e = ref.route_backward(logits.astype(np.float64), idx, d_gate.astype(np.float64), seq, n, want[3],
+                              ref.f64(got["load"]), None, float(np.float32(0.02)), float(np.float32(0.003)))
+    ref.close(d[_t(rest, torch.long)], w[rest], e[rest] + 1e-37)
+    assert torch.isnan(d[10]).all()
+
+
+def test_no_tokens_at_all():
+    logits, idx, _ = _case(12, 16, 2, 1)
+    seq = np.full(12, -1, np.int32)
+    got = _check_loss(logits, idx, seq, 3)
+    assert (got["losses"] == 0).all() and (got["load"] == 0).all() and (got["tokens"] == 0).all()
+    d = torch.full((12, 16), float("nan"), device=device())
+    moe.moe_route_backward(_t(logits), d, tokens=got["tokens"], load=got["load"], seq=_t(seq, I32), z_coef=1.0)
+    assert (d == 0).all()
+
+
+def test_counted_nan_makes_the_losses_nan():
+    logits, idx, _ = _case(12, 16, 2, 1)
+    for v in (np.nan, np.inf):
+        bad = logits.copy()
+        bad[5, 3] = v
+        assert torch.isnan(_loss(_t(bad), _t(idx, I32), None, 1)["losses"]).all()
+
+
+def test_counts_are_those_of_the_routing():
+    """Counts of one sequence without padding are moe_route's, and losses come out the same bits again."""
+    T, E, K = 2000, 200, 6
+    logits = torch.randn((T, E), generator=torch.Generator("cuda").manual_seed(3), device=device())
+    bias = torch.zeros(E, device=device())
+    idx = torch.empty((T, K), dtype=I32, device=device())
+    gate, counts = torch.empty((T, K), device=device()), torch.empty(E, dtype=I32, device=device())
+    moe.moe_route(logits, bias, K, idx, gate, counts)
+    first = _loss(logits, idx, None, 1)
+    assert torch.equal(first["counts"][0], counts) and first["tokens"].tolist() == [T, T]
+    for _ in range(3):
+        again = _loss(logits, idx, None, 1)
+        for k in first:
+            assert torch.equal(first[k], again[k]), k
+
+
+def test_more_tokens_than_blocks_at_a_time():
+    """70,001 tokens: every block has several rows of each wave; many sequences."""
+    logits, idx, seq = _case(70001, 12, 2, 1000)
+    _check_loss(logits, idx, seq, 1000)
+    d = torch.empty((70001, 12), device=device())
+    d_gate = np.random.default_rng(1).standard_normal((70001, 2)).astype(np.float32)
+    moe.moe_route_backward(_t(logits), d, _t(idx, I32), _t(d_gate))
+    part = np.r_[0:50, 8190:8210, 65530:65545, 69980:70001]
+    want, e = ref.route_backward(logits[part].astype(np.float64), idx[part], d_gate[part].astype(np.float64))
+    ref.close(d[_t(part, torch.long)], want, e + 1e-37)

@@ -1,0 +1,216 @@
+"""The norm by mean and variance, the norms that keep their input in 8 bits, and the backward pass of
+both norms, against their 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+import _train as ref
+import sparse_moe_layer_02_amd as moe
+from _parity import device
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+EPS = float(np.float32(1e-5))
+SHAPES = [(1, 8), (1, 6144), (3, 504), (5, 512), (7, 520), (9, 1000), (2, 8192), (3, 8200), (2, 16384),
+          (2, 20008), (1, 32768), (1025, 64), (257, 2048), (2055, 264)]
+
+
+def _t(a, dtype=F32):
+    return torch.as_tensor(np.ascontiguousarray(a), dtype=F32).to(device()).to(dtype)
+
+
+def _x(T, H, dtype, seed=0):
+    """Rows of several sizes, with offsets of up to some of their spread."""
+    rng = np.random.default_rng(H + T + seed)
+    x = (rng.standard_normal((T, H)) + rng.standard_normal((T, 1)) * 2) * np.exp2(rng.integers(-5, 5, (T, 1)))
+    return _t(x, dtype)
+
+
+def _nan(shape, dtype):
+    return torch.full(shape, float("nan"), dtype=dtype, device=device())
+
+
+def _weights(H):
+    rng = np.random.default_rng(H)
+    return _t(1 + 0.2 * rng.standard_normal(H)), _t(rng.standard_normal(H))
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("xt,yt", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_layer_norm(T, H, xt, yt):
+    print(f"\n[case] layer_norm {T}x{H} {xt}->{yt}", flush=True)
+    x = _x(T, H, xt)
+    w, b = _weights(H)
+    for w, b in ((w, b), (w, None), (None, b), (None, None)):
+        y = _nan((T, H), yt)
+        moe.moe_layer_norm(x, w, b, y, EPS)
+        want, e = ref.layer_norm(ref.f64(x), ref.f64(w), ref.f64(b), EPS)
+        ref.close(y, want, ref.rounded(want, e, yt))
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (5, 512), (3, 544), (9, 6144), (2, 8192), (2, 16416), (1, 32768)])
+@pytest.mark.parametrize("xt,yt", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_kept_inputs(T, H, xt, yt):
+    """The norms' outputs are bitwise those without a checkpoint, and the checkpoint that of the conversion."""
+    x = _x(T, H, xt)
+    w, b = _weights(H)
+    want = moe.alloc_checkpoint((T, H))
+    moe.moe_mxfp8_quantize(x, *want)
+    for mean in (False, True):
+        y, z, kept = _nan((T, H), yt), _nan((T, H), yt), moe.alloc_checkpoint((T, H))
+        kept.codes.fill_(1), kept.scales.fill_(1)
+        if mean:
+            moe.moe_layer_norm(x, w, b, y, EPS)
+            moe.moe_layer_norm(x, w, b, z, EPS, checkpoint=kept)
+        else:
+            moe.moe_norm(x, w, y, EPS)
+            moe.moe_norm_checkpoint(x, w, z, kept, EPS)
+        assert torch.equal(y, z)
+        assert torch.equal(kept.codes, want.codes) and torch.equal(kept.scales, want.scales)
+    if xt == yt:                                     # in place
+        moe.moe_norm_checkpoint(x, w, x, kept, EPS)
+        assert torch.equal(kept.codes, want.codes)
+        moe.moe_norm(_x(T, H, xt), w, y, EPS)
+        assert torch.equal(x, y)
+
+
+def _backward(dy, x, w, dx, mean, res=None, eps=EPS, sums=True):
+    T, H = dy.shape
+    dw, db = (_nan((H,), F32), _nan((H,), F32)) if sums else (None, None)
+    ws = torch.full((moe.moe_norm_backward_workspace_bytes(T, H) + 64,), 255, dtype=torch.uint8, device=device())
+    ws_arg = ws[:-64] if sums else None
+    if mean:
+        moe.moe_layer_norm_backward(dy, x, w, dx, dw, db, ws_arg, eps, d_residual=res)
+    else:
+        moe.moe_norm_backward(dy, x, w, dx, dw, ws_arg, eps, d_residual=res)
+    assert (ws[-64:] == 255).all()
+    return dx, dw, db
+
+
+def _check(got, dy, xv, w, mean, res, eps=EPS):
+    (dx, dw, db), (e, e_w, e_b) = ref.norm_backward(ref.f64(dy), xv, ref.f64(w), eps, mean, ref.f64(res))
+    ref.close(got[0], dx, ref.rounded(dx, e, got[0].dtype), "dx")
+    if got[1] is not None:
+        ref.close(got[1], dw, ref.rounded(dw, e_w, F32), "d_weight")
+        if mean:
+            ref.close(got[2], db, ref.rounded(db, e_b, F32), "d_bias")
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("mean", [False, True])
+@pytest.mark.parametrize("dyt,xt,dxt", [(F32, F32, F32), (BF16, BF16, BF16), (BF16, F32, F32), (BF16, F32, BF16),
+                                        (F32, BF16, F32), (F32, F32, BF16), (BF16, BF16, F32), (F32, BF16, BF16)])
+def test_backward(T, H, mean, dyt, xt, dxt):
+    print(f"\n[case] backward {T}x{H} mean={mean} {dyt} {xt} {dxt}", flush=True)
+    rng = np.random.default_rng(T)
+    x, dy = _x(T, H, xt), _t(rng.standard_normal((T, H)), dyt)
+    res = _t(rng.standard_normal((T, H)), dxt)
+    w = _weights(H)[0]
+    for w, res, sums in ((w, res, True), (None, None, True), (w, None, False)):
+        got = _backward(dy, x, w, _nan((T, H), dxt), mean, res, sums=sums)
+        _check(got, dy, ref.f64(x), w, mean, res)
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (5, 512), (3, 544), (300, 1024), (9, 6144), (2, 16416), (1, 32768)])
+@pytest.mark.parametrize("mean", [False, True])
+@pytest.mark.parametrize("dyt,dxt", [(F32, F32), (BF16, BF16), (BF16, F32), (F32, BF16)])
+def test_backward_of_kept_inputs(T, H, mean, dyt, dxt):
+    """From a checkpoint: the gradient at the values that the checkpoint stands for."""
+    print(f"\n[case] backward of kept {T}x{H} mean={mean} {dyt} {dxt}", flush=True)
+    rng = np.random.default_rng(T)
+    kept = moe.alloc_checkpoint((T, H))
+    moe.moe_mxfp8_quantize(_x(T, H, F32), *kept)
+    v = ref.mx8_values(kept.codes.cpu().numpy(), kept.scales.cpu().numpy())
+    dy, res, w = _t(rng.standard_normal((T, H)), dyt), _t(rng.standard_normal((T, H)), dxt), _weights(H)[0]
+    got = _backward(dy, kept, w, _nan((T, H), dxt), mean, res)
+    _check(got, dy, v, w, mean, res)
+    again = _backward(dy, _t(v), w, _nan((T, H), dxt), mean, res)       # and bitwise that of these values
+    for a, b in zip(got, again):
+        if a is not None and not (a is got[2] and not mean):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("mean", [False, True])
+@pytest.mark.parametrize("H", [264, 1000, 8200])
+def test_backward_in_place(mean, H):
+    """dx may be d_residual, x or dy."""
+    T = 21
+    for t in (F32, BF16):
+        x, dy, res, w = _x(T, H, t), _x(T, H, t, 5), _x(T, H, t, 9), _weights(H)[0]
+        want = _backward(dy, x, w, _nan((T, H), t), mean, res)
+        for which in range(3):
+            a = [dy.clone(), x.clone(), res.clone()]
+            got = _backward(a[0], a[1], w, a[which], mean, a[2])
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), which
+
+
+SIZES = [(58, EPS), (64, EPS), (100, EPS), (124, EPS), (124, 0.0), (-50, 0.0), (-70, 0.0), (-70, 1e-35),
+         (-100, 0.0), (-20, EPS)]
+
+
+@pytest.mark.parametrize("T,H", [(5, 8), (5, 504), (5, 1032), (3, 8200), (2, 32768)])
+@pytest.mark.parametrize("mean", [False, True])
+@pytest.mark.parametrize("exp,eps", SIZES)
+def test_rows_of_any_size(T, H, mean, exp, eps):
+    """Sums and squares that fp32 cannot hold; the last row an ordinary one beside them.  dx is taken
+    times the row's size, so that all rows count alike."""
+    print(f"\n[case] any size {T}x{H} mean={mean} 2^{exp} eps {eps}", flush=True)
+    eps = float(np.float32(eps))
+    rng = np.random.default_rng(abs(H + exp))
+    size = np.where(np.arange(T) < T - 1, 2.0 ** exp, 1.0)[:, None]
+    x = _t((rng.standard_normal((T, H)) + 1).clip(-4, 4) * size)
+    w, b = _weights(H)
+    if mean:
+        y = _nan((T, H), F32)
+        moe.moe_layer_norm(x, w, b, y, eps)
+        want, e = ref.layer_norm(ref.f64(x), ref.f64(w), ref.f64(b), eps)
+        ref.close(y, want, ref.rounded(want, e, F32))
+    # gradients of the rows' own size: dx is of order one
+    dy = _t(rng.standard_normal((T, H)) * np.minimum(size, 2.0 ** 100))
+    got = _backward(dy, x, w, _nan((T, H), F32), mean, None, eps, sums=exp < 0)
+    _check(got, dy, ref.f64(x), w, mean, None, eps)
+
+
+def test_rows_that_are_constant_or_not_finite():
+    """A constant row is normed to the bias and has a gradient (eps > 0); a NaN or an infinity stays in
+    its own row of dx."""
+    T, H = 6, 1032
+    x, dy, w = _x(T, H, F32), _x(T, H, F32, 3), _weights(H)[0]
+    x[1], x[2] = 0.5, 0.0                            # 0.5: its mean is exact
+    got = _backward(dy, x, w, _nan((T, H), F32), True)
+    _check(got, dy, ref.f64(x), w, True, None)
+    y = _nan((T, H), F32)
+    moe.moe_layer_norm(x, w, w, y, EPS)
+    assert torch.equal(y[1], w) and torch.equal(y[2], w)
+    clean = _backward(dy, x, w, _nan((T, H), F32), False)[0]
+    x[3, 5], x[4, 1031] = float("nan"), float("inf")
+    for mean in (False, True):
+        dx = _backward(dy, x, w, _nan((T, H), F32), mean)[0]
+        want = clean if not mean else got[0]
+        for t in (0, 1, 2, 5):
+            assert torch.equal(dx[t], want[t])
+        assert torch.isnan(dx[3]).all() and torch.isnan(dx[4]).any()
+        moe.moe_layer_norm(x, w, None, y, EPS)
+        assert torch.isnan(y[3]).all() and torch.isfinite(y[torch.tensor([0, 1, 2, 5])]).all()
+
+
+def test_weight_gradients_of_many_rows_are_the_same_again():
+    """70,000 short rows: each wave has many; the sums are in a fixed order."""
+    T, H = 70000, 72
+    x, dy = _x(T, H, BF16), _x(T, H, BF16, 3)
+    for mean in (False, True):
+        got = _backward(dy, x, None, _nan((T, H), F32), mean)
+        _check(got, dy, ref.f64(x), None, mean, None)
+        for _ in range(3):
+            again = _backward(dy, x, None, _nan((T, H), F32), mean)
+            assert all(torch.equal(a, b) for a, b in zip(got[:2 + mean], again[:2 + mean]))
+
+
+def test_weight_gradient_alone_or_bias_gradient_alone():
+    T, H = 33, 520
+    x, dy, w = _x(T, H, F32), _x(T, H, F32, 3), _weights(H)[0]
+    want = _backward(dy, x, w, _nan((T, H), F32), True)
+    ws = torch.empty(moe.moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=device())
+    for one in (dict(d_weight=_nan((H,), F32)), dict(d_bias=_nan((H,), F32))):
+        moe.moe_layer_norm_backward(dy, x, w, _nan((T, H), F32), ws=ws, eps=EPS, **one)
+        assert torch.equal(list(one.values())[0], want[1] if "d_weight" in one else want[2])
