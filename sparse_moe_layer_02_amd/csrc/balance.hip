@@ -6,15 +6,21 @@
 // is then one sweep over the logits: each row's probabilities times its
 // sequence's loads, so that no sum over tokens is held for every expert of
 // every sequence.  The gradient is one sweep too, a row in registers between
-// its read and its write.  A wave has a row: lane l the experts l + 64 i.
+// its read and its write.  Rows belong to groups of 8 to 64 lanes, by the
+// pool's size, so that a wave has work for its lanes on small pools too.
+#include <algorithm>
+
 #include "train_internal.h"
+#include "wave.h"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
-constexpr int kMaxRowBlocks = 2048;
+constexpr int kCountThreads = 1024;   // at least kMaxRouteE: an expert a thread
+constexpr int kLossThreads = 1024;
+constexpr unsigned kLossBlocks = 256, kGradientBlocks = 4096;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // Sequence of a token, or -1 for padding.
 __device__ __forceinline__ int sequence(const int32_t* seq, int n_seq, long long t) {
@@ -23,38 +29,117 @@ __device__ __forceinline__ int sequence(const int32_t* seq, int n_seq, long long
   return s >= 0 && s < n_seq ? s : -1;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+// ------------------------------------------------------- counts and loads --
+
+// The loads of sequence s by a block of at least E threads: thread e has the
+// expert's picks and group, n tokens.  sum, size: LDS for the groups.
+__device__ __forceinline__ void loads_of(int s, int picks, int g, bool grouped, int n, int E, int K,
+                                         int* sum, int* size, float* load) {
+  const int e = threadIdx.x;
+  const bool in = e < E && g >= 0 && g < E;
+  if (grouped) {
+    if (e < E) sum[e] = size[e] = 0;
+    __syncthreads();
+    if (in) {
+      atomicAdd(&sum[g], picks);
+      atomicAdd(&size[g], 1);
+    }
+    __syncthreads();
+  }
+  if (e >= E) return;
+  const double even = n > 0 ? (double)E / ((double)K * n) : 0.0;
+  float v = 0.0f;
+  if (!grouped)
+    v = (float)(even * picks);
+  else if (in)
+    v = (float)(even * sum[g] / size[g]);
+  load[(size_t)s * E + e] = v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
+
+// Counts and loads in one launch: block s looks at all tokens' sequences, 64
+// tokens to a wave, and counts the picks of those of sequence s in LDS.
+constexpr int kLook = 16;   // windows of 64 tokens whose sequences a wave has in flight
+constexpr int kPicks = 12;  // picks that a lane has in flight
+__global__ __launch_bounds__(kCountThreads) void balance_count_sequence(
+    const int32_t* __restrict__ idx, const int32_t* __restrict__ seq, int n_seq,
+    const int32_t* __restrict__ group, int T, int E, int K, int32_t* __restrict__ counts,
+    int32_t* __restrict__ tokens, float* __restrict__ load, unsigned* __restrict__ ticket) {
+  __shared__ int hist[kMaxRouteE], sum[kMaxRouteE], size[kMaxRouteE];
+  __shared__ int mine, all;
+  const int s = blockIdx.x, lane = threadIdx.x & (kWave - 1), expert = threadIdx.x;
+  const int g = group && expert < E ? group[expert] : expert;
+  hist[expert] = 0;
+  if (threadIdx.x == 0) {
+    mine = all = 0;
+    if (s == 0) *ticket = 0;
+  }
+  __syncthreads();
+  int n = 0, inside = 0;
+  for (int t0 = threadIdx.x / kWave * kWave; t0 < T; t0 += kLook * kCountThreads) {
+    int q[kLook];
 #pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+    for (int u = 0; u < kLook; ++u) {
+      const int t = t0 + u * kCountThreads + lane;
+      q[u] = t < T ? sequence(seq, n_seq, t) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kLook; ++u) {
+      if (t0 + u * kCountThreads >= T) break;
+      const uint64_t here = __ballot(q[u] == s);
+      inside += __popcll(__ballot(q[u] >= 0));
+      n += __popcll(here);
+      if (here == 0) continue;
+      const int32_t* picks = idx + (size_t)(t0 + u * kCountThreads) * K;
+      // bits of tokens past T are not set: their picks are not read
+      for (int i0 = lane; i0 < kWave * K; i0 += kPicks * kWave) {
+        int e[kPicks];
+#pragma unroll
+        for (int k = 0; k < kPicks; ++k) {
+          const int i = i0 + k * kWave;
+          e[k] = i < kWave * K && (here >> (i / K) & 1) ? picks[i] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kPicks; ++k)
+          if (e[k] >= 0 && e[k] < E) atomicAdd(&hist[e[k]], 1);
+      }
+    }
+  }
+  if (lane == 0) {
+    atomicAdd(&mine, n);
+    atomicAdd(&all, inside);
+  }
+  __syncthreads();
+  if (expert < E) counts[(size_t)s * E + expert] = hist[expert];
+  if (threadIdx.x == 0) {
+    tokens[s] = mine;
+    if (s == 0) tokens[n_seq] = all;
+  }
+  loads_of(s, hist[expert], g, group != nullptr, mine, E, K, sum, size, load);
 }
 
 __global__ __launch_bounds__(kThreads) void balance_clear(int32_t* counts, long long n,
-                                                          int32_t* tokens, int n_tokens) {
+                                                          int32_t* tokens, int n_tokens,
+                                                          unsigned* ticket) {
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i < n) counts[i] = 0;
   if (i < n_tokens) tokens[i] = 0;
+  if (i == 0) *ticket = 0;
 }
 
 // A block counts the picks of kCountTokens tokens: those of the first one's
 // sequence, as a rule all of them, in LDS, the others in memory.
-constexpr int kCountThreads = 1024;
 constexpr int kCountTokens = 512;
 __global__ __launch_bounds__(kCountThreads) void balance_count(
     const int32_t* __restrict__ idx, const int32_t* __restrict__ seq, int n_seq, int T, int E,
     int K, int32_t* __restrict__ counts, int32_t* __restrict__ tokens) {
   __shared__ int hist[kMaxRouteE];
-  __shared__ int mine;
+  __shared__ int mine, all;
   const int t0 = blockIdx.x * kCountTokens, n = min(kCountTokens, T - t0);
   const int home = sequence(seq, n_seq, t0);
   for (int e = threadIdx.x; e < E; e += kCountThreads) hist[e] = 0;
-  if (threadIdx.x == 0) mine = 0;
+  if (threadIdx.x == 0) mine = all = 0;
   __syncthreads();
+#pragma unroll 4
   for (int i = threadIdx.x; i < n * K; i += kCountThreads) {
     const int e = idx[(size_t)t0 * K + i], s = sequence(seq, n_seq, t0 + i / K);
     if (e < 0 || e >= E || s < 0) continue;
@@ -66,6 +151,7 @@ __global__ __launch_bounds__(kCountThreads) void balance_count(
   if (threadIdx.x < n) {
     const int s = sequence(seq, n_seq, t0 + threadIdx.x);
     if (s >= 0) {
+      atomicAdd(&all, 1);
       if (s == home)
         atomicAdd(&mine, 1);
       else
@@ -73,164 +159,181 @@ __global__ __launch_bounds__(kCountThreads) void balance_count(
     }
   }
   __syncthreads();
+  if (threadIdx.x == 0 && all) atomicAdd(&tokens[n_seq], all);
   if (home < 0) return;
   for (int e = threadIdx.x; e < E; e += kCountThreads)
     if (hist[e]) atomicAdd(&counts[(size_t)home * E + e], hist[e]);
   if (threadIdx.x == 0 && mine) atomicAdd(&tokens[home], mine);
 }
 
-// A sequence's loads.
-__global__ __launch_bounds__(kThreads) void balance_load(const int32_t* __restrict__ counts,
-                                                         int32_t* __restrict__ tokens, int n_seq,
+__global__ __launch_bounds__(kCountThreads) void balance_load(const int32_t* __restrict__ counts,
+                                                         const int32_t* __restrict__ tokens,
                                                          const int32_t* __restrict__ group, int E,
                                                          int K, float* __restrict__ load) {
   __shared__ int sum[kMaxRouteE], size[kMaxRouteE];
-  const int s = blockIdx.x;
-  const int n = tokens[s];
-  if (s == 0) {   // all tokens
-    __shared__ int all;
-    if (threadIdx.x == 0) all = 0;
-    __syncthreads();
-    int mine = 0;
-    for (int i = threadIdx.x; i < n_seq; i += kThreads) mine += tokens[i];
-    atomicAdd(&all, mine);
-    __syncthreads();
-    if (threadIdx.x == 0) tokens[n_seq] = all;
-  }
-  if (group) {
-    for (int e = threadIdx.x; e < E; e += kThreads) sum[e] = size[e] = 0;
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      const int g = group[e];
-      if (g >= 0 && g < E) {
-        atomicAdd(&sum[g], counts[(size_t)s * E + e]);
-        atomicAdd(&size[g], 1);
-      }
-    }
-    __syncthreads();
-  }
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    float v = 0.0f;
-    if (n > 0) {
-      const double even = (double)E / ((double)K * n);
-      const int g = group ? group[e] : e;
-      if (!group)
-        v = (float)(even * counts[(size_t)s * E + e]);
-      else if (g >= 0 && g < E)
-        v = (float)(even * sum[g] / size[g]);
-    }
-    load[(size_t)s * E + e] = v;
-  }
+  const int s = blockIdx.x, e = threadIdx.x;
+  loads_of(s, e < E ? counts[(size_t)s * E + e] : 0, group && e < E ? group[e] : e,
+           group != nullptr, tokens[s], E, K, sum, size, load);
 }
 
-// A row's probabilities (p, times 1 / the sum) and the logarithm of its sum.
-// A row of -inf alone has zeros.
-template <int EPL>
-struct Softmax {
-  float p[EPL];
-  float lse;
-  __device__ __forceinline__ void row(const float* l, int E, int lane) {
+// ------------------------------------------------------------------ rows --
+
+// A row of E values in the registers of W lanes: N pieces of VEC a lane, piece
+// i of lane l at (i W + l) VEC.
+template <int W, int N, int VEC>
+struct RowOf {
+  static constexpr int kSize = W * N * VEC;
+  static __device__ __forceinline__ int at(int i, int l) { return (i * W + l) * VEC; }
+
+  static __device__ __forceinline__ void load(const float* p, int E, int l, float (&v)[N][VEC],
+                                              float behind) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i][j] = behind;
+      if (at(i, l) < E) {   // VEC divides E
+        if (VEC == 4)
+          *(f32x4*)v[i] = *(const f32x4*)(p + at(i, l));
+        else
+          v[i][0] = p[at(i, l)];
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(float* p, int E, int l, const float (&v)[N][VEC]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (at(i, l) < E) {
+        if (VEC == 4)
+          *(f32x4*)(p + at(i, l)) = *(const f32x4*)v[i];
+        else
+          p[at(i, l)] = v[i][0];
+      }
+  }
+
+  // Logits to probabilities; returns the logarithm of their sum.  A row of -inf
+  // alone gives zeros.  exp is 2^x of a product rounded once: off by the
+  // distance from the largest logit times half a step, beside the sum's own
+  // rounding.
+  static __device__ __forceinline__ float softmax(float (&p)[N][VEC]) {
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + kWave * i;
-      p[i] = e < E ? l[e] : -INFINITY;
-      top = fmaxf(top, p[i]);
-    }
-    top = wave_max(top);
-    // a NaN is no maximum, but leaves none of the sum
-    const float shift = top == -INFINITY ? 0.0f : top;
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      p[i] = expf(p[i] - shift);
-      sum += p[i];
-    }
-    sum = wave_sum(sum);
-    lse = sum == 0.0f ? 0.0f : shift + logf(sum);
+      for (int j = 0; j < VEC; ++j) top = fmaxf(top, p[i][j]);
+    top = group_max<W>(top);
+    if (top == -INFINITY) top = 0.0f;   // (a NaN is no maximum, but leaves none of the sum)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        p[i][j] = __builtin_amdgcn_exp2f((p[i][j] - top) * kLog2e);
+        sum += p[i][j];
+      }
+    sum = group_sum<W>(sum);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) p[i] *= inv;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) p[i][j] *= inv;
+    return sum == 0.0f ? 0.0f : fmaf(__builtin_amdgcn_logf(sum), kLn2, top);
   }
 };
 
-// Per block: the sums over its rows of load p and of lse^2.
-template <int EPL>
-__global__ __launch_bounds__(kThreads) void balance_rows(const float* __restrict__ logits,
-                                                         const int32_t* __restrict__ seq,
-                                                         int n_seq, int T, int E,
-                                                         const float* __restrict__ load,
-                                                         double* __restrict__ sums) {
+// Sums over the rows of load p and of lse^2, a block's to `sums`, and from those
+// the losses, by the block that is the last to have written its own.  What the
+// blocks hand each other passes the caches that they do not share (accesses of
+// agent scope), and a block's sums have arrived (vmcnt 0) before its ticket is
+// drawn: a fence would write back a whole L2 for them, 30 us for 1024 blocks.
+// A ticket costs 7 ns, so the blocks are few and large.
+template <int W, int N, int VEC>
+__global__ __launch_bounds__(kLossThreads) void balance_rows(
+    const float* __restrict__ logits, const int32_t* __restrict__ seq, int n_seq, int T, int E,
+    const float* __restrict__ load, const int32_t* __restrict__ tokens, float balance_coef,
+    float z_coef, double* sums, unsigned* ticket, float* __restrict__ losses) {
+  typedef RowOf<W, N, VEC> Row;
+  constexpr int kRows = kLossThreads / W, kWaves = kLossThreads / kWave;
   __shared__ double part[2][kWaves];
+  __shared__ bool last;
+  const int l = threadIdx.x % W, row = threadIdx.x / W;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  double balance = 0.0, z = 0.0;
-  for (long long t = (long long)blockIdx.x * kWaves + wave; t < T;
-       t += (long long)gridDim.x * kWaves) {
+  double v[2] = {0.0, 0.0};   // in a group's first lane
+  for (long long t = (long long)blockIdx.x * kRows + row; t < T;
+       t += (long long)gridDim.x * kRows) {
     const int s = sequence(seq, n_seq, t);
     if (s < 0) continue;
-    Softmax<EPL> m;
-    m.row(logits + t * E, E, lane);
-    const float* f = load + (size_t)s * E;
+    float p[N][VEC], f[N][VEC];
+    Row::load(logits + t * E, E, l, p, -INFINITY);
+    Row::load(load + (size_t)s * E, E, l, f, 0.0f);
+    const float lse = Row::softmax(p);
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + kWave * i < E) dot = fmaf(m.p[i], f[lane + kWave * i], dot);
-    balance += wave_sum(dot);
-    z += (double)m.lse * m.lse;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) dot = fmaf(p[i][j], f[i][j], dot);
+    dot = group_sum<W>(dot);
+    if (l == 0) {
+      v[0] += dot;
+      v[1] += (double)lse * lse;
+    }
   }
-  if (lane == 0) {
-    part[0][wave] = balance;
-    part[1][wave] = z;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    double v = 0.0;
-    for (int w = 0; w < kWaves; ++w) v += part[threadIdx.x][w];
-    sums[(size_t)blockIdx.x * 2 + threadIdx.x] = v;
-  }
-}
-
-// losses from n blocks' sums.
-__global__ __launch_bounds__(kThreads) void balance_finish(const double* __restrict__ sums, int n,
-                                                           const int32_t* __restrict__ tokens,
-                                                           int n_seq, float balance_coef,
-                                                           float z_coef,
-                                                           float* __restrict__ losses) {
-  __shared__ double part[2][kThreads];
-  double a = 0.0, b = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    a += sums[2 * i];
-    b += sums[2 * i + 1];
-  }
-  part[0][threadIdx.x] = a;
-  part[1][threadIdx.x] = b;
-  __syncthreads();
-  for (int off = kThreads / 2; off > 0; off >>= 1) {
-    if (threadIdx.x < off) {
-      part[0][threadIdx.x] += part[0][threadIdx.x + off];
-      part[1][threadIdx.x] += part[1][threadIdx.x + off];
+  // the waves' sums, then the block's, in thread 0
+  const auto join = [&]() {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int off = kWave / 2; off > 0; off >>= 1) v[k] += __shfl_xor(v[k], off);
+      if (lane == 0) part[k][wave] = v[k];
     }
     __syncthreads();
+    if (threadIdx.x == 0)
+      for (int k = 0; k < 2; ++k) {
+        v[k] = 0.0;
+        for (int w = 0; w < kWaves; ++w) v[k] += part[k][w];
+      }
+  };
+  join();
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 2; ++k)
+      __hip_atomic_store(&sums[2 * blockIdx.x + k], v[k], __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::: "memory");
+    wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+           gridDim.x - 1;
   }
+  __syncthreads();
+  if (!last) return;
+  for (int k = 0; k < 2; ++k)
+    v[k] = threadIdx.x < gridDim.x   // kLossBlocks of them at most
+               ? __hip_atomic_load(&sums[2 * threadIdx.x + k], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT)
+               : 0.0;
+  join();
   if (threadIdx.x == 0) {
     const int all = tokens[n_seq];
-    losses[0] = all > 0 ? (float)(balance_coef * part[0][0] / all) : 0.0f;
-    losses[1] = all > 0 ? (float)(z_coef * part[1][0] / all) : 0.0f;
+    losses[0] = all > 0 ? (float)(balance_coef * v[0] / all) : 0.0f;
+    losses[1] = all > 0 ? (float)(z_coef * v[1] / all) : 0.0f;
   }
 }
 
-// d_logits may be logits: a wave has read the row that it overwrites.
-template <int EPL>
+// d_logits may be logits: a group has read the row that it overwrites.
+template <int W, int N, int VEC>
 __global__ __launch_bounds__(kThreads) void route_backward(
     const float* logits, const int32_t* __restrict__ idx, const float* __restrict__ d_gate,
     const int32_t* __restrict__ seq, int n_seq, const int32_t* __restrict__ tokens,
     const float* __restrict__ load, const float* __restrict__ d_losses, float balance_coef,
     float z_coef, int T, int E, int K, float* d_logits) {
-  __shared__ float gates[kWaves][kWave * EPL];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  float* mine = gates[wave];
+  typedef RowOf<W, N, VEC> Row;
+  constexpr int kRows = kThreads / W;   // rows of a block at a time
+  __shared__ __attribute__((aligned(16))) float gates[kThreads * N * VEC];
+  const int l = threadIdx.x % W, row = threadIdx.x / W;
+  float* mine = gates + row * Row::kSize;   // the gates' gradient by expert, zeros between rows
   if (d_gate) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) mine[lane + kWave * i] = 0.0f;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) mine[Row::at(i, l) + j] = 0.0f;
   }
   float cb = 0.0f, cz = 0.0f;
   if (load) {
@@ -240,99 +343,139 @@ __global__ __launch_bounds__(kThreads) void route_backward(
       cz = 2.0f * z_coef * (d_losses ? d_losses[1] : 1.0f) / (float)all;
     }
   }
-  for (long long t = (long long)blockIdx.x * kWaves + wave; t < T;
-       t += (long long)gridDim.x * kWaves) {
-    Softmax<EPL> m;
-    m.row(logits + t * E, E, lane);
-    float g[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) g[i] = 0.0f;
+  for (long long t = (long long)blockIdx.x * kRows + row; t < T;
+       t += (long long)gridDim.x * kRows) {
+    float p[N][VEC], g[N][VEC], f[N][VEC];
+    Row::load(logits + t * E, E, l, p, -INFINITY);
+    const int s = load ? sequence(seq, n_seq, t) : -1;
+    if (s >= 0) Row::load(load + (size_t)s * E, E, l, f, 0.0f);
     if (d_gate) {
-      // the picks one after the other: equal ones add up in their order
-      for (int k0 = 0; k0 < K; k0 += kWave) {
-        const int k = k0 + lane;
-        const int e = k < K ? idx[t * K + k] : -1;
+      wave_lds_order();
+      for (int k0 = 0; k0 < K; k0 += W) {
+        const int k = k0 + l;
+        int e = k < K ? idx[t * K + k] : -1;
         const float d = k < K ? d_gate[t * K + k] : 0.0f;
-        for (int j = 0; j < min(kWave, K - k0); ++j) {
-          if (lane == j && e >= 0 && e < E) mine[e] += d;
-          wave_lds_sync();
+        if (e >= E) e = -1;
+        // whether two picks of the row are one expert: its lanes' numbers meet
+        bool alone = K <= W;
+        if (alone) {
+          if (e >= 0) mine[e] = __int_as_float(l);
+          wave_lds_order();
+          alone = __ballot(e >= 0 && __float_as_int(mine[e]) != l) == 0;
+          wave_lds_order();
+          if (e >= 0) mine[e] = alone ? d : 0.0f;
+          wave_lds_order();
         }
+        if (!alone)   // one after the other: equal picks add up in their order
+          for (int j = 0; j < W; ++j) {
+            if (l == j && e >= 0) mine[e] += d;
+            wave_lds_order();
+          }
       }
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        g[i] = mine[lane + kWave * i];
-        mine[lane + kWave * i] = 0.0f;
-      }
-      wave_lds_sync();
-    }
-    float more = 0.0f;
-    if (load) {
-      const int s = sequence(seq, n_seq, t);
-      if (s >= 0) {
-        const float* f = load + (size_t)s * E;
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (lane + kWave * i < E) g[i] = fmaf(cb, f[lane + kWave * i], g[i]);
-        more = cz * m.lse;
+        for (int j = 0; j < VEC; ++j) g[i][j] = mine[Row::at(i, l) + j];
+      wave_lds_order();
+      for (int k = l; k < K; k += W) {
+        const int e = idx[t * K + k];
+        if (e >= 0 && e < E) mine[e] = 0.0f;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) g[i][j] = 0.0f;
     }
+    const float lse = Row::softmax(p);
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      if (m.p[i] == 0.0f) g[i] = 0.0f;   // a masked pick's gradient may be anything
-      dot = fmaf(m.p[i], g[i], dot);
-    }
-    dot = wave_sum(dot);
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + kWave * i < E) d_logits[t * E + lane + kWave * i] = m.p[i] * (g[i] - dot + more);
+      for (int j = 0; j < VEC; ++j) {
+        if (p[i][j] == 0.0f) g[i][j] = 0.0f;   // a masked pick's gradient may be anything
+        if (s >= 0) g[i][j] = fmaf(cb, f[i][j], g[i][j]);
+        dot = fmaf(p[i][j], g[i][j], dot);
+      }
+    dot = group_sum<W>(dot);
+    const float more = s >= 0 ? cz * lse : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) p[i][j] *= g[i][j] - dot + more;
+    Row::store(d_logits + t * E, E, l, p);
   }
 }
 
-unsigned row_blocks(int T) { return min(ceil_div(T, kWaves), (unsigned)kMaxRowBlocks); }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// The narrowest groups of lanes that hold a row, four values a lane and load
+// where rows and pointers allow.
+#define MOE_ROW_SHAPE(E, vec4, CALL)        \
+  do {                                      \
+    if (vec4) {                             \
+      if ((E) <= 32) CALL(8, 1, 4);         \
+      else if ((E) <= 64) CALL(16, 1, 4);   \
+      else if ((E) <= 128) CALL(32, 1, 4);  \
+      else if ((E) <= 256) CALL(64, 1, 4);  \
+      else if ((E) <= 512) CALL(64, 2, 4);  \
+      else if ((E) <= 768) CALL(64, 3, 4);  \
+      else CALL(64, 4, 4);                  \
+    } else {                                \
+      if ((E) <= 8) CALL(8, 1, 1);          \
+      else if ((E) <= 16) CALL(16, 1, 1);   \
+      else if ((E) <= 32) CALL(32, 1, 1);   \
+      else if ((E) <= 64) CALL(64, 1, 1);   \
+      else if ((E) <= 128) CALL(64, 2, 1);  \
+      else if ((E) <= 256) CALL(64, 4, 1);  \
+      else if ((E) <= 512) CALL(64, 8, 1);  \
+      else if ((E) <= 768) CALL(64, 12, 1); \
+      else CALL(64, 16, 1);                 \
+    }                                       \
+  } while (0)
+
+constexpr size_t kTicketBytes = 256;
+constexpr long long kSequencePicks = 32768, kSequenceTokens = 1 << 20;
 
 }  // namespace
 
 size_t balance_ws_bytes(int T, int E, int n_seq) {
   (void)E;
   (void)n_seq;
-  return (size_t)row_blocks(T) * 2 * sizeof(double);
+  (void)T;
+  return kTicketBytes + kLossBlocks * 2 * sizeof(double);
 }
-
-#define MOE_BY_WIDTH(E, CALL)             \
-  do {                                    \
-    const int epl = ((E) + kWave - 1) / kWave; \
-    if (epl <= 1) CALL(1);                \
-    else if (epl <= 2) CALL(2);           \
-    else if (epl <= 4) CALL(4);           \
-    else if (epl <= 8) CALL(8);           \
-    else if (epl <= 12) CALL(12);         \
-    else CALL(16);                        \
-  } while (0)
 
 hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* seq,
                                int n_seq, const int32_t* group, int T, int E, int K,
                                float balance_coef, float z_coef, int32_t* counts, int32_t* tokens,
                                float* load, float* losses, void* ws, hipStream_t s) {
-  const long long n = (long long)n_seq * E;
-  double* sums = (double*)ws;
-  const unsigned blocks = row_blocks(T);
-  MOE_LAUNCH("balance_clear", s,
-             balance_clear<<<ceil_div((size_t)max(n, (long long)n_seq + 1), kThreads), kThreads, 0,
-                             s>>>(counts, n, tokens, n_seq + 1));
-  MOE_LAUNCH("balance_count", s,
-             balance_count<<<ceil_div(T, kCountTokens), kCountThreads, 0, s>>>(
-                 idx, seq, n_seq, T, E, K, counts, tokens));
-  MOE_LAUNCH("balance_load", s,
-             balance_load<<<n_seq, kThreads, 0, s>>>(counts, tokens, n_seq, group, E, K, load));
-#define MOE_BALANCE(EPL)                                                                    \
-  MOE_LAUNCH("balance_rows", s,                                                             \
-             balance_rows<EPL><<<blocks, kThreads, 0, s>>>(logits, seq, n_seq, T, E, load, sums))
-  MOE_BY_WIDTH(E, MOE_BALANCE);
+  unsigned* ticket = (unsigned*)ws;
+  double* sums = (double*)((char*)ws + kTicketBytes);
+  // one launch where an even sequence's picks are few enough for one block
+  if ((long long)T * K <= kSequencePicks * n_seq && (long long)T * n_seq <= kSequenceTokens) {
+    MOE_LAUNCH("balance_count", s,
+               balance_count_sequence<<<n_seq, kCountThreads, 0, s>>>(
+                   idx, seq, n_seq, group, T, E, K, counts, tokens, load, ticket));
+  } else {
+    const long long n = std::max((long long)n_seq * E, (long long)n_seq + 1);
+    MOE_LAUNCH("balance_clear", s,
+               balance_clear<<<ceil_div(n, kThreads), kThreads, 0, s>>>(
+                   counts, (long long)n_seq * E, tokens, n_seq + 1, ticket));
+    MOE_LAUNCH("balance_count", s,
+               balance_count<<<ceil_div(T, kCountTokens), kCountThreads, 0, s>>>(
+                   idx, seq, n_seq, T, E, K, counts, tokens));
+    MOE_LAUNCH("balance_load", s,
+               balance_load<<<n_seq, kCountThreads, 0, s>>>(counts, tokens, group, E, K, load));
+  }
+#define MOE_BALANCE(W, N, VEC)                                                                 \
+  MOE_LAUNCH("balance_rows", s,                                                                \
+             balance_rows<W, N, VEC>                                                           \
+                 <<<std::min(ceil_div(T, kLossThreads / W), kLossBlocks), kLossThreads, 0, s>>>( \
+                     logits, seq, n_seq, T, E, load, tokens, balance_coef, z_coef, sums,       \
+                     ticket, losses))
+  MOE_ROW_SHAPE(E, E % 4 == 0 && aligned16(logits) && aligned16(load), MOE_BALANCE);
 #undef MOE_BALANCE
-  MOE_LAUNCH("balance_finish", s,
-             balance_finish<<<1, kThreads, 0, s>>>(sums, blocks, tokens, n_seq, balance_coef,
-                                                   z_coef, losses));
   return hipGetLastError();
 }
 
@@ -341,12 +484,14 @@ hipError_t launch_route_backward(const float* logits, const int32_t* idx, const 
                                  const float* load, const float* d_losses, float balance_coef,
                                  float z_coef, int T, int E, int K, float* d_logits,
                                  hipStream_t s) {
-#define MOE_BACKWARD(EPL)                                                                   \
-  MOE_LAUNCH("route_backward", s,                                                           \
-             route_backward<EPL><<<row_blocks(T), kThreads, 0, s>>>(                        \
-                 logits, idx, d_gate, seq, n_seq, tokens, load, d_losses, balance_coef,     \
-                 z_coef, T, E, K, d_logits))
-  MOE_BY_WIDTH(E, MOE_BACKWARD);
+#define MOE_BACKWARD(W, N, VEC)                                                                \
+  MOE_LAUNCH("route_backward", s,                                                              \
+             route_backward<W, N, VEC>                                                         \
+                 <<<std::min(ceil_div(T, kThreads / W), kGradientBlocks), kThreads, 0, s>>>(   \
+                     logits, idx, d_gate, seq, n_seq, tokens, load, d_losses, balance_coef,    \
+                     z_coef, T, E, K, d_logits))
+  MOE_ROW_SHAPE(E, E % 4 == 0 && aligned16(logits) && aligned16(load) && aligned16(d_logits),
+                MOE_BACKWARD);
 #undef MOE_BACKWARD
   return hipGetLastError();
 }
