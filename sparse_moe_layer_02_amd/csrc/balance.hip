@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void balance_clear(int32_t* counts, long 
 
 // A block counts the picks of kCountTokens tokens: those of the first one's
 // sequence, as a rule all of them, in LDS, the others in memory.
-constexpr int kCountTokens = 512;
+constexpr int kCountTokens = 256;
 __global__ __launch_bounds__(kCountThreads) void balance_count(
     const int32_t* __restrict__ idx, const int32_t* __restrict__ seq, int n_seq, int T, int E,
     int K, int32_t* __restrict__ counts, int32_t* __restrict__ tokens) {
@@ -452,8 +452,8 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const in
                                float* load, float* losses, void* ws, hipStream_t s) {
   unsigned* ticket = (unsigned*)ws;
   double* sums = (double*)((char*)ws + kTicketBytes);
-  // one launch where an even sequence's picks are few enough for one block
-  if ((long long)T * K <= kSequencePicks * n_seq && (long long)T * n_seq <= kSequenceTokens) {
+  // one launch where a block may count all picks and look at all tokens
+  if ((long long)T * K <= kSequencePicks && (long long)T * n_seq <= kSequenceTokens) {
     MOE_LAUNCH("balance_count", s,
                balance_count_sequence<<<n_seq, kCountThreads, 0, s>>>(
                    idx, seq, n_seq, group, T, E, K, counts, tokens, load, ticket));
