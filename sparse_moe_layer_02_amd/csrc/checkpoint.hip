@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kThreads) void mxfp8_quantize(const T* __restrict__
   float v[8];
   Row8<T>::load(x + i * 8, v);
   unsigned byte;
-  codes[i] = mx8::encode(v, byte);
+  codes[i] = mx8::encode<8>(v, byte);
   if ((i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kThreads) void mxfp8_dequantize(
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n8) return;
   float v[8];
-  mx8::decode(codes[i], scales[i >> 2], v);
+  mx8::decode<8>(codes[i], scales[i >> 2], v);
   Row8<T>::store(y + i * 8, v);
 }
 
@@ -66,9 +66,9 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const T* __restrict__ 
   Row8<T>::store(hh + i * 8, h);
   if (SAVE) {
     unsigned byte;
-    codes[at] = mx8::encode(g, byte);
+    codes[at] = mx8::encode<8>(g, byte);
     if ((at & 3) == 0) scales[at >> 2] = (uint8_t)byte;
-    codes[at + row8] = mx8::encode(u, byte);
+    codes[at + row8] = mx8::encode<8>(u, byte);
     if ((at & 3) == 0) scales[(at + row8) >> 2] = (uint8_t)byte;
   }
 }
@@ -85,8 +85,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
   Row8<T>::load(d_hh + i * 8, d);
   if (SAVED) {
     const mx8::u32x2* codes = (const mx8::u32x2*)gu;
-    mx8::decode(codes[at], scales[at >> 2], g);
-    mx8::decode(codes[at + row8], scales[(at + row8) >> 2], u);
+    mx8::decode<8>(codes[at], scales[at >> 2], g);
+    mx8::decode<8>(codes[at + row8], scales[(at + row8) >> 2], u);
   } else {
     Row8<T>::load((const T*)gu + at * 8, g);
     Row8<T>::load((const T*)gu + (at + row8) * 8, u);

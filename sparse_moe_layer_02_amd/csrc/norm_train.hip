@@ -10,6 +10,8 @@
 // Its blocks go over many rows each and keep the weights' gradients of their
 // rows in registers; the blocks' sums are joined by a second kernel in a fixed
 // order.
+#include <type_traits>
+
 #include "mx8.h"
 #include "norm_rows.h"
 #include "train_internal.h"
@@ -23,56 +25,76 @@ namespace {
 
 constexpr int kMaxWaves = kMaxThreads / kWave;
 
-// A row's 8 values as they are kept: loaded early as Raw, taken apart later.
+// VEC values of a row as they are kept: loaded early as Raw, taken apart later.
 // arrived: a point that the load is waited for at, before any that follow it.
-template <typename T> struct Source;
-template <> struct Source<bf16> {
-  typedef bf16x8 Raw;
+// Loads go past the caches, rows are read once (8192 rows of 6144, bf16, from
+// 8-bit rows: 72 us with the default policy, 58 so).  Rows with fp32 among them
+// are held in pieces of 4 values, so that every load and store of a wave has
+// whole lines; others in pieces of 8.
+typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
+template <typename T, int VEC> struct Source;
+template <int VEC> struct Source<bf16, VEC> {
+  typedef __attribute__((__vector_size__(VEC * sizeof(__bf16)))) __bf16 Raw;
   const bf16* p;
   static __device__ __forceinline__ void arrived(Raw& r) { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ Raw load(size_t at) const { return *(const bf16x8*)(p + at); }
+  __device__ __forceinline__ Raw load(size_t at) const {
+    return __builtin_nontemporal_load((const Raw*)(p + at));
+  }
   static __device__ __forceinline__ void values(const Raw& r, float* v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)r[i];
+    for (int i = 0; i < VEC; ++i) v[i] = (float)r[i];
   }
 };
-template <> struct Source<float> {
-  struct Raw {
-    f32x4 a, b;
-  };
+template <> struct Source<float, 4> {
+  typedef f32x4 Raw;
   const float* p;
-  static __device__ __forceinline__ void arrived(Raw& r) {
-    asm volatile("" : "+v"(r.a), "+v"(r.b));
-  }
+  static __device__ __forceinline__ void arrived(Raw& r) { asm volatile("" : "+v"(r)); }
   __device__ __forceinline__ Raw load(size_t at) const {
-    return Raw{*(const f32x4*)(p + at), *(const f32x4*)(p + at + 4)};
+    return __builtin_nontemporal_load((const f32x4*)(p + at));
   }
   static __device__ __forceinline__ void values(const Raw& r, float* v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = r.a[i];
-      v[4 + i] = r.b[i];
-    }
+    for (int i = 0; i < 4; ++i) v[i] = r[i];
   }
 };
 struct Mx8;
-template <> struct Source<Mx8> {
+template <int VEC> struct Source<Mx8, VEC> {
+  typedef mx8::Codes<VEC> Codes;
   struct Raw {
-    mx8::u32x2 codes;
+    Codes codes;
     unsigned scale;
   };
+  const uint8_t* codes;
+  const uint8_t* scales;
   static __device__ __forceinline__ void arrived(Raw& r) {
     asm volatile("" : "+v"(r.codes), "+v"(r.scale));
   }
-  const uint8_t* codes;
-  const uint8_t* scales;
   __device__ __forceinline__ Raw load(size_t at) const {
-    return Raw{*(const mx8::u32x2*)(codes + at), scales[at / 32]};
+    return Raw{__builtin_nontemporal_load((const Codes*)(codes + at)), scales[at / 32]};
   }
   static __device__ __forceinline__ void values(const Raw& r, float* v) {
-    mx8::decode(r.codes, r.scale, v);
+    mx8::decode<VEC>(r.codes, r.scale, v);
   }
 };
+
+template <int VEC> __device__ __forceinline__ void load_floats(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < VEC; i += 4) *(f32x4*)(v + i) = *(const f32x4*)(p + i);
+}
+template <int VEC> __device__ __forceinline__ void store_floats(float* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < VEC; i += 4) *(f32x4*)(p + i) = *(const f32x4*)(v + i);
+}
+// VEC values past the caches.
+template <int VEC> __device__ __forceinline__ void store_past(bf16* p, const float* o) {
+  typename Source<bf16, VEC>::Raw v;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] = (bf16)o[i];
+  __builtin_nontemporal_store(v, (typename Source<bf16, VEC>::Raw*)p);
+}
+template <int VEC> __device__ __forceinline__ void store_past(float* p, const float* o) {
+  __builtin_nontemporal_store(f32x4{o[0], o[1], o[2], o[3]}, (f32x4*)p);
+}
 
 // Sums of N values over the threads of a row.  part: LDS of their own, zero
 // where there are fewer than WAVES waves.
@@ -98,56 +120,23 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[WAVES]) {
   }
 }
 
-// Whether piece p of a thread lies in the row.
-__device__ __forceinline__ bool inside(int p, int H) {
-  return (p * (int)blockDim.x + (int)threadIdx.x) * 8 < H;
-}
-
 // Rows whose sums leave fp32's range, as inv_rms has them.
 __device__ __forceinline__ bool too_large(float ss) { return !(ss < __builtin_inff()); }
 __device__ __forceinline__ bool too_small(float ss, float eps) {
   return ss < 0x1p-90f && eps < 0x1p-100f;
 }
 
-// v = v - mean(v), and the sum of its squares: part of 2 sums.
-template <int P>
-__device__ __forceinline__ float deviations(float (&v)[P][8], int H, float (*part)[kMaxWaves]) {
-  float s[1] = {0.0f};
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-    if (inside(p, H))
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += v[p][i];
-  row_sums<kMaxWaves>(s, part);
-  const float m = s[0] / (float)H;
-  s[0] = 0.0f;
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-    if (inside(p, H))
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[p][i] -= m;
-        s[0] = fmaf(v[p][i], v[p][i], s[0]);
-      }
-  row_sums<kMaxWaves>(s, part + 1);
-  return s[0];
-}
-
-// MEAN: by mean and variance; else y is that of norm_kernel, bit for bit.
-// SAVE: x in 8 bits to codes and scales (a row's pieces of 4 neighbouring
-// threads are a block of 32).
-template <typename T, typename U, int P, bool MEAN, bool SAVE>
-__global__ __launch_bounds__(kMaxThreads) void norm_save_kernel(
-    const T* x, const float* __restrict__ w, const float* __restrict__ b, float eps, int rows,
-    int H, U* y, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  __shared__ float part[4][kMaxWaves];
+// The root mean square norm that keeps its input: y is that of norm_kernel, bit
+// for bit (the same threads hold the same values and join their sums in the
+// same order), and a row's pieces of 4 neighbouring threads are a block of 32.
+template <typename T, typename U, int P>
+__global__ __launch_bounds__(kMaxThreads) void norm_checkpoint_kernel(
+    const T* x, const float* __restrict__ w, float eps, int rows, int H, U* y,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  __shared__ float part[2][kMaxWaves];
   const bool one_wave = blockDim.x == kWave;
   const unsigned t = row_of_thread();
   if (t >= (unsigned)rows) return;   // a whole wave, and then blocks have no barrier
-  if (MEAN && !one_wave) {
-    if (threadIdx.x < 4 * kMaxWaves) part[threadIdx.x / kMaxWaves][threadIdx.x % kMaxWaves] = 0.0f;
-    lds_barrier();
-  }
   float v[P][8];
   float ss = 0.0f;
 #pragma unroll
@@ -156,50 +145,14 @@ __global__ __launch_bounds__(kMaxThreads) void norm_save_kernel(
     if (h < H) {
       const size_t at = (size_t)t * H + h;
       Row8<T>::load(x + at, v[p]);
-      if (SAVE) {
-        unsigned byte;
-        *(mx8::u32x2*)(codes + at) = mx8::encode(v[p], byte);
-        if ((threadIdx.x & 3) == 0) scales[at / 32] = (uint8_t)byte;
-      }
+      unsigned byte;
+      *(mx8::Codes<8>*)(codes + at) = mx8::encode<8>(v[p], byte);
+      if ((threadIdx.x & 3) == 0) scales[at / 32] = (uint8_t)byte;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(v[p][i], v[p][i], ss);
     }
   }
-  float r;
-  if (MEAN) {
-    ss = deviations(v, H, part);
-    float f = 1.0f;
-    if (too_large(ss)) {
-      // the deviations may be lost too: the values again, scaled
-      f = 0x1p-96f;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int h = (p * blockDim.x + threadIdx.x) * 8;
-        if (h < H) {
-          Row8<T>::load(x + (size_t)t * H + h, v[p]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[p][i] *= f;
-        }
-      }
-      ss = deviations(v, H, part + 2);
-    } else if (too_small(ss, eps)) {
-      f = 0x1p96f;
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        if (inside(p, H))
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[p][i] *= f;
-            s[0] = fmaf(v[p][i], v[p][i], s[0]);
-          }
-      row_sums<kMaxWaves>(s, part + 2);
-      ss = s[0];
-    }
-    r = rsqrtf(ss / (float)H + eps * f * f);
-  } else {
-    r = inv_rms(v, ss, eps, H, part, one_wave);
-  }
+  const float r = inv_rms(v, ss, eps, H, part, one_wave);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int h = (p * blockDim.x + threadIdx.x) * 8;
@@ -208,31 +161,170 @@ __global__ __launch_bounds__(kMaxThreads) void norm_save_kernel(
       if (w) Row8<float>::load(w + h, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[p][i] = v[p][i] * r * g[i];
-      if (MEAN && b) {
-        Row8<float>::load(b + h, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] += g[i];
-      }
       Row8<U>::store(y + (size_t)t * H + h, v[p]);
     }
   }
 }
 
-// A block goes over the rows blockIdx.x * blockDim.y + threadIdx.y, and so on;
-// a row has THREADS threads at most, of P pieces each.  sum_w, sum_b: the
-// block's sums over its rows go to row blockIdx.x of them, `stride` floats a
-// row; NULL: not asked for.
-// Up to 8192 values a row has at most 256 threads, with the weight in registers
-// and the next row's x and dy in flight while one is worked on: what a row costs
-// once (its sums, addresses) is shared by up to 32 values a lane, and two or
-// three blocks of a CU wait for different things.  Longer rows have neither.
-template <typename DY, typename X, typename DX, int P, int THREADS, bool MEAN>
-__global__ __launch_bounds__(THREADS) void norm_backward_kernel(
-    Source<DY> dy, Source<X> x, const float* __restrict__ w, float eps, int rows, int H,
-    Source<DX> d_residual, DX* dx, float* __restrict__ sum_w, float* __restrict__ sum_b,
+// Pieces of a row in a thread: piece p starts at at[p].  Only the last pieces,
+// kLoose of them, may lie behind the row (row_shape sees to it): in[] for those.
+// Loads are made for all pieces, from the row's start for one that is behind: a
+// load under a condition would be waited for where it is made, to be merged
+// with what was there.
+template <int P, int VEC> struct Pieces {
+  static constexpr int kLoose = 8 / VEC, kFirst = P - kLoose;
+  int at[P];
+  bool in[kLoose];
+  __device__ __forceinline__ Pieces(int H) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      at[p] = (p * (int)blockDim.x + (int)threadIdx.x) * VEC;
+      if (p >= kFirst) {
+        in[p - kFirst] = at[p] < H;
+        if (at[p] >= H) at[p] = 0;
+      }
+    }
+  }
+  __device__ __forceinline__ bool inside(int p) const { return p < kFirst || in[p - kFirst]; }
+  // behind the row: nothing to any sum
+  __device__ __forceinline__ void clear_behind(float (&v)[P][VEC]) const {
+#pragma unroll
+    for (int p = kFirst; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[p][i] = in[p - kFirst] ? v[p][i] : 0.0f;
+  }
+};
+
+// v = v - mean(v).
+template <int WAVES, int P, int VEC>
+__device__ __forceinline__ void center(float (&v)[P][VEC], const Pieces<P, VEC>& pieces,
+                                       int H, float (*part)[WAVES]) {
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[0] += v[p][i];
+  row_sums<WAVES>(s, part);
+  const float m = s[0] / (float)H;   // exact where the row's values are equal
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[p][i] -= m;
+  pieces.clear_behind(v);
+}
+
+// The sum of v's squares.
+template <int WAVES, int P, int VEC>
+__device__ __forceinline__ float squares(const float (&v)[P][VEC], float (*part)[WAVES]) {
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[0] = fmaf(v[p][i], v[p][i], s[0]);
+  row_sums<WAVES>(s, part);
+  return s[0];
+}
+
+template <int P, int VEC> __device__ __forceinline__ void scale(float (&v)[P][VEC], float f) {
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[p][i] *= f;
+}
+
+// SAVE: x in 8 bits to codes and scales too; the pieces of 32 / VEC neighbouring
+// threads are a block.
+template <typename T, typename U, int P, int VEC, int THREADS, bool SAVE>
+__global__ __launch_bounds__(THREADS) void layer_norm_kernel(
+    Source<T, VEC> x, const float* __restrict__ w, const float* __restrict__ b, float eps,
+    int rows, int H, U* y, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr int kWaves = THREADS <= 256 ? 4 : 16;
+  __shared__ __attribute__((aligned(16))) float part[4][kWaves];
+  if (blockDim.y == 1) {
+    if (threadIdx.x < 4 * kWaves) (&part[0][0])[threadIdx.x] = 0.0f;
+    lds_barrier();
+  }
+  const unsigned t = row_of_thread();
+  if (t >= (unsigned)rows) return;   // a whole wave, and then blocks have no barrier
+  const size_t row = (size_t)t * H;
+  const Pieces<P, VEC> pieces(H);
+  const float inv_h = 1.0f / (float)H;
+  float v[P][VEC];
+  const auto load = [&]() {
+    typename Source<T, VEC>::Raw raw[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) raw[p] = x.load(row + pieces.at[p]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) Source<T, VEC>::values(raw[p], v[p]);
+  };
+  load();
+  if (SAVE) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      unsigned byte;
+      const mx8::Codes<VEC> c = mx8::encode<VEC>(v[p], byte);
+      if (pieces.inside(p)) {   // all lanes of a block or none
+        const size_t at = row + pieces.at[p];
+        __builtin_nontemporal_store(c, (mx8::Codes<VEC>*)(codes + at));
+        if (pieces.at[p] % 32 == 0) scales[at / 32] = (uint8_t)byte;
+      }
+    }
+  }
+  pieces.clear_behind(v);
+  center(v, pieces, H, part);
+  float ss = squares(v, part + 1), f = 1.0f;
+  if (too_large(ss)) {
+    f = 0x1p-96f;
+    load();   // the deviations may be lost already
+    pieces.clear_behind(v);
+    scale(v, f);
+    center(v, pieces, H, part + 2);
+    ss = squares(v, part + 3);
+  } else if (too_small(ss, eps)) {
+    f = 0x1p96f;
+    scale(v, f);
+    ss = squares(v, part + 2);
+  }
+  const float r = rsqrtf(ss * inv_h + eps * f * f);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    float g[VEC];
+    if (w) {
+      load_floats<VEC>(w + pieces.at[p], g);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[p][i] = v[p][i] * r * g[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[p][i] *= r;
+    }
+    if (b) {
+      load_floats<VEC>(b + pieces.at[p], g);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[p][i] += g[i];
+    }
+    if (pieces.inside(p)) store_past<VEC>(y + row + pieces.at[p], v[p]);
+  }
+}
+
+// A block goes over the rows blockIdx.x * blockDim.y + threadIdx.y, and so on.
+// sum_w, sum_b: the block's sums over its rows go to row blockIdx.x of them,
+// `stride` floats a row; NULL: not asked for.
+// Up to 12288 values a row's threads have the weight in registers and the next
+// row's x and dy in flight while one is worked on: what a row costs once (its
+// sums, addresses) is shared by up to 24 values a lane, and the blocks of a CU
+// wait for different things.  Longer rows have neither.
+template <typename DY, typename X, typename DX, int P, int VEC, int THREADS, bool MEAN>
+__global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward_kernel(
+    Source<DY, VEC> dy, Source<X, VEC> x, const float* __restrict__ w, float eps, int rows, int H,
+    Source<DX, VEC> d_residual, DX* dx, float* __restrict__ sum_w, float* __restrict__ sum_b,
     int stride) {
-  constexpr bool kAhead = THREADS <= 256;
-  constexpr int kSums = 9, kWaves = THREADS / kWave < 16 ? 4 : 16;
+  constexpr bool kAhead = THREADS <= 512;
+  constexpr int kSums = 9, kWaves = THREADS <= 256 ? 4 : 16;
+  // the weights' gradients of a thread's columns: in registers, or, where these
+  // do not hold them for two waves a SIMD, in LDS that is the thread's alone
+  constexpr bool kInLds = kAhead && P * VEC > 16;
+  __shared__ __attribute__((aligned(16))) float acc[kInLds ? 2 : 1][kInLds ? P : 1]
+                                                   [kInLds ? THREADS : 1][VEC];
   // the sums of one row are read while those of the next are written
   __shared__ __attribute__((aligned(16))) float part[2][kSums][kWaves];
   for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 2 * kSums * kWaves;
@@ -241,87 +333,73 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(
   __syncthreads();
   const long long step = (long long)gridDim.x * blockDim.y;
   long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-  // Only a thread's last piece may lie behind the row (the shape sees to it).
-  // Loads are made for all pieces, from the row's start for one that is behind
-  // and from the last row for one that is no more: a load under a condition
-  // would be waited for where it is made, to be merged with what was there.
-  const bool last_in = inside(P - 1, H);
+  const Pieces<P, VEC> pieces(H);
   const float inv_h = 1.0f / (float)H;
-  int at[P];
-  float dw[P][8] = {}, db[P][8] = {}, weight[kAhead ? P : 1][8];
+  float dw[P][VEC] = {}, db[P][VEC] = {};
+  if (kInLds) {
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-    at[p] = p < P - 1 || last_in ? (p * (int)blockDim.x + (int)threadIdx.x) * 8 : 0;
-  const auto weights = [&](int p, float (&g)[8]) {
+    for (int p = 0; p < P; ++p) {
+      store_floats<VEC>(acc[0][p][threadIdx.x], dw[p]);
+      store_floats<VEC>(acc[1][p][threadIdx.x], db[p]);
+    }
+  }
+  float weight[kAhead ? P : 1][VEC];
+  const auto weights = [&](int p, float (&g)[VEC]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = 1.0f;
-    if (w) Row8<float>::load(w + at[p], g);
+    for (int i = 0; i < VEC; ++i) g[i] = 1.0f;
+    if (w) load_floats<VEC>(w + pieces.at[p], g);
   };
-  typename Source<DY>::Raw next_dy[P];
-  typename Source<X>::Raw next_x[P];
+  typename Source<DY, VEC>::Raw next_dy[P];
+  typename Source<X, VEC>::Raw next_x[P];
+  // (from the last row where there is no next one)
   const auto fetch = [&](long long row) {
     const size_t start = (size_t)min(row, (long long)rows - 1) * H;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      next_x[p] = x.load(start + at[p]);
-      next_dy[p] = dy.load(start + at[p]);
+      next_x[p] = x.load(start + pieces.at[p]);
+      next_dy[p] = dy.load(start + pieces.at[p]);
+    }
+  };
+  const auto arrived = [&]() {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      Source<X, VEC>::arrived(next_x[p]);
+      Source<DY, VEC>::arrived(next_dy[p]);
     }
   };
   if (kAhead) {
 #pragma unroll
     for (int p = 0; p < P; ++p) weights(p, weight[p]);
     fetch(t);
+    arrived();
   }
   for (int turn = 0; t < rows; t += step, turn ^= 1) {
     const size_t row = (size_t)t * H;
-    float v[P][8], d[P][8];   // x, then its deviations; dy
-    typename Source<DX>::Raw res[P];
+    float v[P][VEC], d[P][VEC];   // x, then its deviations; dy
+    typename Source<DX, VEC>::Raw res[P];
     if (!kAhead) fetch(t);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      Source<X>::arrived(next_x[p]);
-      Source<DY>::arrived(next_dy[p]);
-      Source<X>::values(next_x[p], v[p]);
-      Source<DY>::values(next_dy[p], d[p]);
+      Source<X, VEC>::values(next_x[p], v[p]);
+      Source<DY, VEC>::values(next_dy[p], d[p]);
     }
     if (d_residual.p) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) res[p] = d_residual.load(row + at[p]);
+      for (int p = 0; p < P; ++p) res[p] = d_residual.load(row + pieces.at[p]);
     }
     if (kAhead) fetch(t + step);
-    // behind the row: nothing to any sum
-    const auto clear_behind = [&](float (&a)[P][8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[P - 1][i] = last_in ? a[P - 1][i] : 0.0f;
-    };
-    clear_behind(v);
-    clear_behind(d);
+    pieces.clear_behind(v);
+    pieces.clear_behind(d);
     float s[3];
-    // v = v - mean(v)
-    const auto center = [&](float (*lds)[kWaves]) {
-      if (!MEAN) return;
-      float a[1] = {0.0f};
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[0] += v[p][i];
-      row_sums<kWaves>(a, lds);
-      const float m = a[0] * inv_h;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] -= m;
-      clear_behind(v);
-    };
     // the squares of v, g times v, and g
     const auto sums = [&](float (*lds)[kWaves]) {
       s[0] = s[1] = s[2] = 0.0f;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        float g[8];
+        float g[VEC];
         if (!kAhead) weights(p, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < VEC; ++i) {
           const float gi = d[p][i] * (kAhead ? weight[p][i] : g[i]);
           s[0] = fmaf(v[p][i], v[p][i], s[0]);
           s[1] = fmaf(gi, v[p][i], s[1]);
@@ -337,7 +415,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(
         s[1] = two[1];
       }
     };
-    center(part[turn]);
+    if (MEAN) center(v, pieces, H, part[turn]);
     sums(part[turn] + 1);
     // n = v to_n, dx = (..) root f
     float f = 1.0f, root = rsqrtf(s[0] * inv_h + eps), to_n = root;
@@ -345,72 +423,78 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(
       // rare, and the same for the row's threads: v scaled, then normed before it meets g
       const bool large = too_large(s[0]);
       f = large ? 0x1p-96f : too_small(s[0], eps) ? 0x1p96f : 1.0f;
-      float a[1] = {0.0f};
       if (large) {   // the deviations may be lost already
 #pragma unroll
-        for (int p = 0; p < P; ++p) Source<X>::values(x.load(row + at[p]), v[p]);
-        clear_behind(v);
+        for (int p = 0; p < P; ++p) Source<X, VEC>::values(x.load(row + pieces.at[p]), v[p]);
+        pieces.clear_behind(v);
       }
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] *= f;
-      if (large) center(part[turn] + 4);
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[0] = fmaf(v[p][i], v[p][i], a[0]);
-      row_sums<kWaves>(a, part[turn] + 5);
-      root = rsqrtf(a[0] * inv_h + eps * f * f);
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] *= root;
+      scale(v, f);
+      if (MEAN && large) center(v, pieces, H, part[turn] + 4);
+      root = rsqrtf(squares(v, part[turn] + 5) * inv_h + eps * f * f);
+      scale(v, root);
       to_n = 1.0f;
       sums(part[turn] + 6);
     }
+    // the next row's loads end here, so that nothing waits for this row's stores
+    if (kAhead) arrived();
     const float c = to_n * s[1] * inv_h, mean_g = MEAN ? s[2] * inv_h : 0.0f;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      float g[8], o[8] = {};
+      float g[VEC], o[VEC] = {};
       if (!kAhead) weights(p, g);
-      if (d_residual.p) Source<DX>::values(res[p], o);
+      if (d_residual.p) Source<DX, VEC>::values(res[p], o);
+      if (kInLds) {
+        load_floats<VEC>(acc[0][p][threadIdx.x], dw[p]);
+        load_floats<VEC>(acc[1][p][threadIdx.x], db[p]);
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < VEC; ++i) {
         const float n = v[p][i] * to_n, gi = d[p][i] * (kAhead ? weight[p][i] : g[i]);
         o[i] = fmaf((gi - mean_g - n * c) * root, f, o[i]);   // root f may pass 2^128
         dw[p][i] = fmaf(d[p][i], n, dw[p][i]);
         db[p][i] += d[p][i];
       }
-      if (p < P - 1 || last_in) Row8<DX>::store(dx + row + at[p], o);
+      if (kInLds) {
+        store_floats<VEC>(acc[0][p][threadIdx.x], dw[p]);
+        if (MEAN) store_floats<VEC>(acc[1][p][threadIdx.x], db[p]);
+      }
+      if (pieces.inside(p)) store_past<VEC>(dx + row + pieces.at[p], o);
     }
   }
   if (!sum_w && !sum_b) return;
-  if (P == 1 && kAhead && blockDim.y > 1) {
+  if (P * VEC == 8 && blockDim.y > 1) {
     // the block's rows at a time share a column: joined in their order
     __shared__ float other[3][2][kWave * 8];
     if (threadIdx.y > 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        other[threadIdx.y - 1][0][i * kWave + threadIdx.x] = dw[0][i];
-        other[threadIdx.y - 1][1][i * kWave + threadIdx.x] = db[0][i];
-      }
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          other[threadIdx.y - 1][0][(p * VEC + i) * kWave + threadIdx.x] = dw[p][i];
+          other[threadIdx.y - 1][1][(p * VEC + i) * kWave + threadIdx.x] = db[p][i];
+        }
     }
     __syncthreads();
     if (threadIdx.y > 0) return;
     for (int y = 1; y < (int)blockDim.y; ++y)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dw[0][i] += other[y - 1][0][i * kWave + threadIdx.x];
-        db[0][i] += other[y - 1][1][i * kWave + threadIdx.x];
-      }
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          dw[p][i] += other[y - 1][0][(p * VEC + i) * kWave + threadIdx.x];
+          db[p][i] += other[y - 1][1][(p * VEC + i) * kWave + threadIdx.x];
+        }
   }
 #pragma unroll
   for (int p = 0; p < P; ++p)
-    if (p < P - 1 || last_in) {
-      const size_t to = (size_t)blockIdx.x * stride + at[p];
-      if (sum_w) Row8<float>::store(sum_w + to, dw[p]);
-      if (MEAN && sum_b) Row8<float>::store(sum_b + to, db[p]);
+    if (pieces.inside(p)) {
+      if (kInLds) {
+        load_floats<VEC>(acc[0][p][threadIdx.x], dw[p]);
+        load_floats<VEC>(acc[1][p][threadIdx.x], db[p]);
+      }
+      const size_t to = (size_t)blockIdx.x * stride + pieces.at[p];
+      if (sum_w) store_floats<VEC>(sum_w + to, dw[p]);
+      if (MEAN && sum_b) store_floats<VEC>(sum_b + to, db[p]);
     }
 }
 
@@ -446,17 +530,30 @@ __global__ __launch_bounds__(kWave* kJoinWaves) void join_sums(const float* __re
   out[h] = v;
 }
 
-// The backward pass's blocks: four rows of a wave each, or a row of a block.
-Shape backward_shape(int T, int H) {
+// Threads of a row, P pieces of 8 values each: up to 6144 values at most 256
+// threads, four rows of a wave to a block where that is enough for one; up to
+// 12288 at most 512.
+// (P - 1) * 8 values for every thread lie inside the row: Pieces counts on it.
+Shape row_shape(int T, int H) {
   Shape s;
-  s.P = std::min(ceil_div(H, 2048), 4u);
+  s.P = H <= 6144 ? ceil_div(H, 2048) : H <= 12288 ? ceil_div(H, 4096) : 4;
   const int per = ceil_div(ceil_div(H, 8 * s.P), kWave) * kWave;
-  const int rows = per == kWave ? 4 : 1;
-  s.block = dim3(per, rows);
-  // blocks for two waves a SIMD, each with a few rows
-  const unsigned most = 256 * std::max(1, 512 / (per * rows));
-  s.grid = dim3(std::min(ceil_div(T, rows), most));
+  s.block = dim3(per, per == kWave ? 4 : 1);
+  const unsigned blocks = ceil_div(T, s.block.y);
+  s.grid.x = std::min(blocks, kMaxGridX);
+  s.grid.y = ceil_div(blocks, s.grid.x);
   return s;
+}
+// The backward pass's blocks: for two waves a SIMD, each with a few rows.
+Shape backward_shape(int T, int H) {
+  Shape s = row_shape(T, H);
+  const unsigned most = 256 * std::max(1u, 512 / (s.block.x * s.block.y));
+  s.grid = dim3(std::min(ceil_div(T, s.block.y), most));
+  return s;
+}
+// Values of a piece: 4 where there is fp32 among the types, else 8.
+template <typename... T> constexpr int piece_of() {
+  return (std::is_same<T, float>::value || ...) ? 4 : 8;
 }
 
 }  // namespace
@@ -467,63 +564,96 @@ size_t norm_backward_ws_bytes(int T, int H) {
 
 namespace {
 
-template <typename T, typename U>
-void save_t(bool mean, const void* x, const float* w, const float* b, float eps, int T_, int H,
-            void* y, uint8_t* codes, uint8_t* scales, hipStream_t st) {
-  const Shape s = shape(T_, H);
-#define MOE_NORM(P, MEAN, SAVE)                                                               \
-  MOE_LAUNCH(MEAN ? "layer_norm" : "norm_checkpoint", st,                                     \
-             norm_save_kernel<T, U, P, MEAN, SAVE><<<s.grid, s.block, 0, st>>>(               \
-                 (const T*)x, w, b, eps, T_, H, (U*)y, codes, scales))
-#define MOE_NORM_P(MEAN, SAVE) \
-  if (s.P == 1)                \
-    MOE_NORM(1, MEAN, SAVE);   \
-  else if (s.P == 2)           \
-    MOE_NORM(2, MEAN, SAVE);   \
-  else                         \
-    MOE_NORM(4, MEAN, SAVE);
-  if (!mean) {
-    MOE_NORM_P(false, true)
-  } else if (codes) {
-    MOE_NORM_P(true, true)
-  } else {
-    MOE_NORM_P(true, false)
+// CALL(P, THREADS) for a row shape.
+#define MOE_ROW_P(H, s, CALL)   \
+  if ((H) <= 6144) {            \
+    if ((s).P == 1)             \
+      CALL(1, 256);             \
+    else if ((s).P == 2)        \
+      CALL(2, 256);             \
+    else                        \
+      CALL(3, 256);             \
+  } else if ((H) <= 12288) {    \
+    if ((s).P == 2)             \
+      CALL(2, 512);             \
+    else                        \
+      CALL(3, 512);             \
+  } else {                      \
+    CALL(4, 1024);              \
   }
-#undef MOE_NORM_P
+
+template <typename T, typename U>
+void checkpoint_t(const void* x, const float* w, float eps, int T_, int H, void* y,
+                  uint8_t* codes, uint8_t* scales, hipStream_t st) {
+  const Shape s = shape(T_, H);
+#define MOE_NORM(P)                                                                       \
+  MOE_LAUNCH("norm_checkpoint", st,                                                       \
+             norm_checkpoint_kernel<T, U, P><<<s.grid, s.block, 0, st>>>(                 \
+                 (const T*)x, w, eps, T_, H, (U*)y, codes, scales))
+  if (s.P == 1)
+    MOE_NORM(1);
+  else if (s.P == 2)
+    MOE_NORM(2);
+  else
+    MOE_NORM(4);
 #undef MOE_NORM
 }
 
+template <typename T, typename U>
+void layer_norm_t(const void* x, const float* w, const float* b, float eps, int T_, int H,
+                  void* y, uint8_t* codes, uint8_t* scales, hipStream_t st) {
+  const Shape s = row_shape(T_, H);
+  constexpr int VEC = piece_of<T, U>();
+#define MOE_NORM(P, THREADS, SAVE)                                                            \
+  MOE_LAUNCH("layer_norm", st,                                                                \
+             layer_norm_kernel<T, U, P * 8 / VEC, VEC, THREADS, SAVE>                         \
+                 <<<s.grid, s.block, 0, st>>>(Source<T, VEC>{(const T*)x}, w, b, eps, T_, H, \
+                                              (U*)y, codes, scales))
+#define MOE_SAVE(P, THREADS) MOE_NORM(P, THREADS, true)
+#define MOE_PLAIN(P, THREADS) MOE_NORM(P, THREADS, false)
+  if (codes) {
+    MOE_ROW_P(H, s, MOE_SAVE)
+  } else {
+    MOE_ROW_P(H, s, MOE_PLAIN)
+  }
+#undef MOE_PLAIN
+#undef MOE_SAVE
+#undef MOE_NORM
+}
+
+// x: the rows or codes, x_scales with codes.
+template <typename X, int VEC> Source<X, VEC> source_of(const void* x, const uint8_t* x_scales) {
+  if constexpr (std::is_same<X, Mx8>::value)
+    return Source<X, VEC>{(const uint8_t*)x, x_scales};
+  else
+    return Source<X, VEC>{(const X*)x};
+}
+
 template <typename DY, typename X, typename DX>
-void backward_t(bool mean, const void* dy, Source<X> x, const float* w, float eps, int T, int H,
-                const void* d_residual, void* dx, float* d_weight, float* d_bias, float* ws,
-                hipStream_t st) {
+void backward_t(bool mean, const void* dy, const void* x, const uint8_t* x_scales, const float* w,
+                float eps, int T, int H, const void* d_residual, void* dx, float* d_weight,
+                float* d_bias, float* ws, hipStream_t st) {
   const Shape s = backward_shape(T, H);
+  constexpr int VEC = piece_of<DY, X, DX>();
   // one block has the whole sums
   const bool join = s.grid.x > 1 && (d_weight || d_bias);
   float* sum_w = join ? ws : d_weight;
   float* sum_b = join ? ws + H : d_bias;
-#define MOE_NORM(P, THREADS, MEAN)                                                           \
-  MOE_LAUNCH("norm_backward", st,                                                            \
-             norm_backward_kernel<DY, X, DX, P, THREADS, MEAN><<<s.grid, s.block, 0, st>>>(  \
-                 Source<DY>{(const DY*)dy}, x, w, eps, T, H, Source<DX>{(const DX*)d_residual}, \
-                 (DX*)dx, sum_w, sum_b, 2 * H))
-#define MOE_NORM_P(MEAN)         \
-  if (H > 8192)                  \
-    MOE_NORM(4, 1024, MEAN);     \
-  else if (s.P == 1)             \
-    MOE_NORM(1, 256, MEAN);      \
-  else if (s.P == 2)             \
-    MOE_NORM(2, 256, MEAN);      \
-  else if (s.P == 3)             \
-    MOE_NORM(3, 256, MEAN);      \
-  else                           \
-    MOE_NORM(4, 256, MEAN);
+#define MOE_NORM(P, THREADS, MEAN)                                                            \
+  MOE_LAUNCH("norm_backward", st,                                                             \
+             norm_backward_kernel<DY, X, DX, P * 8 / VEC, VEC, THREADS, MEAN>                 \
+                 <<<s.grid, s.block, 0, st>>>(                                                \
+                     Source<DY, VEC>{(const DY*)dy}, source_of<X, VEC>(x, x_scales), w, eps, T, \
+                     H, Source<DX, VEC>{(const DX*)d_residual}, (DX*)dx, sum_w, sum_b, 2 * H))
+#define MOE_MEAN(P, THREADS) MOE_NORM(P, THREADS, true)
+#define MOE_ROOT(P, THREADS) MOE_NORM(P, THREADS, false)
   if (mean) {
-    MOE_NORM_P(true)
+    MOE_ROW_P(H, s, MOE_MEAN)
   } else {
-    MOE_NORM_P(false)
+    MOE_ROW_P(H, s, MOE_ROOT)
   }
-#undef MOE_NORM_P
+#undef MOE_ROOT
+#undef MOE_MEAN
 #undef MOE_NORM
   if (join)
     MOE_LAUNCH("norm_join_sums", st,
@@ -535,15 +665,16 @@ template <typename DY, typename DX>
 void backward_x(bool mean, const void* dy, const void* x, int x_dtype, const uint8_t* x_scales,
                 const float* w, float eps, int T, int H, const void* d_residual, void* dx,
                 float* d_weight, float* d_bias, float* ws, hipStream_t st) {
+#define MOE_BACK(X)                                                                         \
+  backward_t<DY, X, DX>(mean, dy, x, x_scales, w, eps, T, H, d_residual, dx, d_weight, d_bias, \
+                        ws, st)
   if (x_scales)
-    backward_t<DY, Mx8, DX>(mean, dy, Source<Mx8>{(const uint8_t*)x, x_scales}, w, eps, T, H,
-                            d_residual, dx, d_weight, d_bias, ws, st);
+    MOE_BACK(Mx8);
   else if (x_dtype == MOE_BF16)
-    backward_t<DY, bf16, DX>(mean, dy, Source<bf16>{(const bf16*)x}, w, eps, T, H, d_residual, dx,
-                             d_weight, d_bias, ws, st);
+    MOE_BACK(bf16);
   else
-    backward_t<DY, float, DX>(mean, dy, Source<float>{(const float*)x}, w, eps, T, H, d_residual,
-                              dx, d_weight, d_bias, ws, st);
+    MOE_BACK(float);
+#undef MOE_BACK
 }
 
 }  // namespace
@@ -551,7 +682,9 @@ void backward_x(bool mean, const void* dy, const void* x, int x_dtype, const uin
 hipError_t launch_norm_save(bool mean, const void* x, int x_dtype, const float* weight,
                             const float* bias, float eps, int T, int H, void* y, int y_dtype,
                             uint8_t* codes, uint8_t* scales, hipStream_t s) {
-#define MOE_SAVE(T_, U) save_t<T_, U>(mean, x, weight, bias, eps, T, H, y, codes, scales, s)
+#define MOE_SAVE(T_, U)                                                                \
+  (mean ? layer_norm_t<T_, U>(x, weight, bias, eps, T, H, y, codes, scales, s)         \
+        : checkpoint_t<T_, U>(x, weight, eps, T, H, y, codes, scales, s))
   if (x_dtype == MOE_BF16)
     y_dtype == MOE_BF16 ? MOE_SAVE(bf16, bf16) : MOE_SAVE(bf16, float);
   else

@@ -13,6 +13,11 @@ __device__ __forceinline__ float dpp_of(float v) {
       __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
 }
 
+template <int CTRL>
+__device__ __forceinline__ unsigned dpp_of(unsigned v) {
+  return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+
 // The values of the lanes 16 or 32 apart, as a pair whose order is the same for both.
 __device__ __forceinline__ void swap16(float v, float& a, float& b) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,

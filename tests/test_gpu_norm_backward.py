@@ -124,7 +124,8 @@ def test_backward_of_kept_inputs(T, H, mean, dyt, dxt):
     dy, res, w = _t(rng.standard_normal((T, H)), dyt), _t(rng.standard_normal((T, H)), dxt), _weights(H)[0]
     got = _backward(dy, kept, w, _nan((T, H), dxt), mean, res)
     _check(got, dy, v, w, mean, res)
-    again = _backward(dy, _t(v), w, _nan((T, H), dxt), mean, res)       # and bitwise that of these values
+    # and bitwise that of these values in bf16, which holds them
+    again = _backward(dy, _t(v, BF16), w, _nan((T, H), dxt), mean, res)
     for a, b in zip(got, again):
         if a is not None and not (a is got[2] and not mean):
             assert torch.equal(a, b)
