@@ -12,89 +12,18 @@
 // order.
 #include <type_traits>
 
-#include "mx8.h"
 #include "norm_rows.h"
+#include "stream.h"
 #include "train_internal.h"
-#include "wave.h"
 
 namespace moe {
 
 using namespace norms;
+using namespace stream;
 
 namespace {
 
 constexpr int kMaxWaves = kMaxThreads / kWave;
-
-// VEC values of a row as they are kept: loaded early as Raw, taken apart later.
-// arrived: a point that the load is waited for at, before any that follow it.
-// Loads go past the caches, rows are read once (8192 rows of 6144, bf16, from
-// 8-bit rows: 72 us with the default policy, 58 so).  Rows with fp32 among them
-// are held in pieces of 4 values, so that every load and store of a wave has
-// whole lines; others in pieces of 8.
-typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4;
-template <typename T, int VEC> struct Source;
-template <int VEC> struct Source<bf16, VEC> {
-  typedef __attribute__((__vector_size__(VEC * sizeof(__bf16)))) __bf16 Raw;
-  const bf16* p;
-  static __device__ __forceinline__ void arrived(Raw& r) { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ Raw load(size_t at) const {
-    return __builtin_nontemporal_load((const Raw*)(p + at));
-  }
-  static __device__ __forceinline__ void values(const Raw& r, float* v) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = (float)r[i];
-  }
-};
-template <> struct Source<float, 4> {
-  typedef f32x4 Raw;
-  const float* p;
-  static __device__ __forceinline__ void arrived(Raw& r) { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ Raw load(size_t at) const {
-    return __builtin_nontemporal_load((const f32x4*)(p + at));
-  }
-  static __device__ __forceinline__ void values(const Raw& r, float* v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = r[i];
-  }
-};
-struct Mx8;
-template <int VEC> struct Source<Mx8, VEC> {
-  typedef mx8::Codes<VEC> Codes;
-  struct Raw {
-    Codes codes;
-    unsigned scale;
-  };
-  const uint8_t* codes;
-  const uint8_t* scales;
-  static __device__ __forceinline__ void arrived(Raw& r) {
-    asm volatile("" : "+v"(r.codes), "+v"(r.scale));
-  }
-  __device__ __forceinline__ Raw load(size_t at) const {
-    return Raw{__builtin_nontemporal_load((const Codes*)(codes + at)), scales[at / 32]};
-  }
-  static __device__ __forceinline__ void values(const Raw& r, float* v) {
-    mx8::decode<VEC>(r.codes, r.scale, v);
-  }
-};
-
-template <int VEC> __device__ __forceinline__ void load_floats(const float* p, float* v) {
-#pragma unroll
-  for (int i = 0; i < VEC; i += 4) *(f32x4*)(v + i) = *(const f32x4*)(p + i);
-}
-template <int VEC> __device__ __forceinline__ void store_floats(float* p, const float* v) {
-#pragma unroll
-  for (int i = 0; i < VEC; i += 4) *(f32x4*)(p + i) = *(const f32x4*)(v + i);
-}
-// VEC values past the caches.
-template <int VEC> __device__ __forceinline__ void store_past(bf16* p, const float* o) {
-  typename Source<bf16, VEC>::Raw v;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = (bf16)o[i];
-  __builtin_nontemporal_store(v, (typename Source<bf16, VEC>::Raw*)p);
-}
-template <int VEC> __device__ __forceinline__ void store_past(float* p, const float* o) {
-  __builtin_nontemporal_store(f32x4{o[0], o[1], o[2], o[3]}, (f32x4*)p);
-}
 
 // Sums of N values over the threads of a row.  part: LDS of their own, zero
 // where there are fewer than WAVES waves.
@@ -161,7 +90,12 @@ __global__ __launch_bounds__(kMaxThreads) void norm_checkpoint_kernel(
       if (w) Row8<float>::load(w + h, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[p][i] = v[p][i] * r * g[i];
-      Row8<U>::store(y + (size_t)t * H + h, v[p]);
+      // past the caches, which then have the codes for the backward pass (113 -> 110 us
+      // both ways, 8192 x 6144); fp32 in pieces of 8 would be half lines
+      if constexpr (std::is_same<U, bf16>::value)
+        store_past<8>(y + (size_t)t * H + h, v[p]);
+      else
+        Row8<U>::store(y + (size_t)t * H + h, v[p]);
     }
   }
 }
@@ -550,10 +484,6 @@ Shape backward_shape(int T, int H) {
   const unsigned most = 256 * std::max(1u, 512 / (s.block.x * s.block.y));
   s.grid = dim3(std::min(ceil_div(T, s.block.y), most));
   return s;
-}
-// Values of a piece: 4 where there is fp32 among the types, else 8.
-template <typename... T> constexpr int piece_of() {
-  return (std::is_same<T, float>::value || ...) ? 4 : 8;
 }
 
 }  // namespace
