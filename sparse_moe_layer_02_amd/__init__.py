@@ -66,6 +66,8 @@ class MoEError(RuntimeError):
 def lib():
     """The loaded shared library (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -95,19 +97,21 @@ def _check(fn: str, status: int):
 
 
 def _dev(*ts):
-    d = None
+    # by device numbers: comparing torch.device objects costs more than all else here
+    d = first = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()
+        if i < 0:
             raise ValueError("tensors must live on the GPU")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
         if d is None:
-            d = t.device
-        elif t.device != d:
+            d, first = i, t
+        elif i != d:
             raise ValueError("tensors on different devices")
-    return d
+    return None if first is None else first.device
 
 
 def _want(t, dtype, name):

@@ -38,8 +38,10 @@ def _call(name, device, *args):
     a Stream object around it, no device switch where there is none to make."""
     f = getattr(lib(), name)
     i = device.index
-    if i == torch.cuda.current_device():
-        _check(name, f(*args, torch._C._cuda_getCurrentRawStream(i)))
+    if i == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(i))
+        if status:
+            _check(name, status)
     else:
         with torch.cuda.device(i):
             _check(name, f(*args, torch._C._cuda_getCurrentRawStream(i)))

@@ -5,8 +5,10 @@
 // All are sweeps bound by memory: a thread takes 8 values, as one piece or two,
 // and the pieces of 32 / VEC neighbouring lanes are a block of 32 (a block never
 // crosses a row, and rows are contiguous).  Everything goes past the caches but
-// the codes that are written: what reads them next is the backward pass, and of a
-// smaller batch they are still there.
+// the codes that are written, which the backward pass finds there of a smaller
+// batch, and the values that are converted alone, which another kernel has just
+// written (8192 x 2048 fp32 13.0 us so, 15.7 past the caches; 8192 x 6144 bf16
+// 28.4 and 27.3).
 #include "stream.h"
 #include "train_internal.h"
 
@@ -49,7 +51,7 @@ __global__ __launch_bounds__(kThreads) void mxfp8_quantize(Source<T, piece_of<T>
     const long long g = group_of<VEC>(u);
     if (g < end) {   // all lanes of a block or none
       float v[VEC];
-      Source<T, VEC>::values(x.load(g * VEC), v);
+      Source<T, VEC>::values(*(const typename Source<T, VEC>::Raw*)(x.p + g * VEC), v);
       store_codes<VEC>(v, g, codes, scales);
     }
   }
