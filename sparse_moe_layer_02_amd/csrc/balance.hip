@@ -199,14 +199,16 @@ struct RowOf {
       }
     }
   }
+  // Past the caches (16384 x 768: 17.7 us the gradient's pass, 22.4 with the default
+  // policy; loads past them 23.4).
   static __device__ __forceinline__ void store(float* p, int E, int l, const float (&v)[N][VEC]) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (at(i, l) < E) {
         if (VEC == 4)
-          *(f32x4*)(p + at(i, l)) = *(const f32x4*)v[i];
+          __builtin_nontemporal_store(*(const f32x4*)v[i], (f32x4*)(p + at(i, l)));
         else
-          p[at(i, l)] = v[i][0];
+          __builtin_nontemporal_store(v[i][0], p + at(i, l));
       }
   }
 

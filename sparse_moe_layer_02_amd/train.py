@@ -50,19 +50,21 @@ def alloc_checkpoint(shape, device="cuda"):
 
 def _mx8(codes, scales, shape, name):
     """Check that codes and scales are MXFP8 rows of this shape."""
-    _want(codes, torch.uint8, name)
-    _want(scales, torch.uint8, name)
-    _require(shape[-1] % BLOCK == 0 and tuple(codes.shape) == tuple(shape) and
-             tuple(scales.shape) == (*shape[:-1], shape[-1] // BLOCK),
-             f"{name}: codes [..., C] and scales [..., C / 32] of its tensor's shape")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError(f"{name}: expected codes and scales of {torch.uint8}")
+    cols = shape[-1]
+    if cols % BLOCK or codes.shape != shape or scales.shape != (*shape[:-1], cols // BLOCK):
+        raise ValueError(f"argument check failed: {name}: codes [..., C] and scales [..., C / 32] "
+                         "of its tensor's shape")
 
 
 def _kept(checkpoint, shape):
     """codes and scales of a checkpoint to be written, or two None."""
     if checkpoint is None:
         return None, None
-    _mx8(*checkpoint, shape, "checkpoint")
-    return checkpoint
+    codes, scales = checkpoint
+    _mx8(codes, scales, shape, "checkpoint")
+    return codes, scales
 
 
 def _rows(n_rows):
