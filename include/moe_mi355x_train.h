@@ -135,7 +135,7 @@ moe_status moe_layer_norm(const void *x, int x_dtype, const float *weight, const
  * of the same dtype.  d_weight [H] fp32, or NULL where the weight has no
  * gradient (ws may then be NULL).
  * fp32 arithmetic; d_weight is a sum over rows in a fixed order that depends
- * on T and H alone.
+ * on the sizes, the types and whether there is a d_residual.
  * MOE_ERR_SHAPE: T < 1, H < 1, H % 8 (MXFP8: H % 32), H > 32768, or eps
  * negative or not finite.  MOE_ERR_ALIGN: 16 bytes, x_scales 4, ws 256.
  * ws: at least moe_norm_backward_workspace_bytes(T, H). */

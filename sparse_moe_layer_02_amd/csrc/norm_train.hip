@@ -55,51 +55,6 @@ __device__ __forceinline__ bool too_small(float ss, float eps) {
   return ss < 0x1p-90f && eps < 0x1p-100f;
 }
 
-// The root mean square norm that keeps its input: y is that of norm_kernel, bit
-// for bit (the same threads hold the same values and join their sums in the
-// same order), and a row's pieces of 4 neighbouring threads are a block of 32.
-template <typename T, typename U, int P>
-__global__ __launch_bounds__(kMaxThreads) void norm_checkpoint_kernel(
-    const T* x, const float* __restrict__ w, float eps, int rows, int H, U* y,
-    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  __shared__ float part[2][kMaxWaves];
-  const bool one_wave = blockDim.x == kWave;
-  const unsigned t = row_of_thread();
-  if (t >= (unsigned)rows) return;   // a whole wave, and then blocks have no barrier
-  float v[P][8];
-  float ss = 0.0f;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int h = (p * blockDim.x + threadIdx.x) * 8;
-    if (h < H) {
-      const size_t at = (size_t)t * H + h;
-      Row8<T>::load(x + at, v[p]);
-      unsigned byte;
-      *(mx8::Codes<8>*)(codes + at) = mx8::encode<8>(v[p], byte);
-      if ((threadIdx.x & 3) == 0) scales[at / 32] = (uint8_t)byte;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[p][i], v[p][i], ss);
-    }
-  }
-  const float r = inv_rms(v, ss, eps, H, part, one_wave);
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int h = (p * blockDim.x + threadIdx.x) * 8;
-    if (h < H) {
-      float g[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-      if (w) Row8<float>::load(w + h, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] = v[p][i] * r * g[i];
-      // past the caches, which then have the codes for the backward pass (113 -> 110 us
-      // both ways, 8192 x 6144); fp32 in pieces of 8 would be half lines
-      if constexpr (std::is_same<U, bf16>::value)
-        store_past<8>(y + (size_t)t * H + h, v[p]);
-      else
-        Row8<U>::store(y + (size_t)t * H + h, v[p]);
-    }
-  }
-}
-
 // Pieces of a row in a thread: piece p starts at at[p].  Only the last pieces,
 // kLoose of them, may lie behind the row (row_shape sees to it): in[] for those.
 // Loads are made for all pieces, from the row's start for one that is behind: a
@@ -128,6 +83,111 @@ template <int P, int VEC> struct Pieces {
       for (int i = 0; i < VEC; ++i) v[p][i] = in[p - kFirst] ? v[p][i] : 0.0f;
   }
 };
+
+// 8 values of a row in the order in which norm_kernel has them.
+template <typename T> struct Eight;
+template <> struct Eight<bf16> : Source<bf16, 8> {
+  __device__ __forceinline__ Raw load(size_t at) const { return *(const Raw*)(p + at); }
+};
+template <> struct Eight<float> {
+  struct Raw {
+    f32x4 a, b;
+  };
+  const float* p;
+  static __device__ __forceinline__ void arrived(Raw& r) {
+    asm volatile("" : "+v"(r.a), "+v"(r.b));
+  }
+  // (through the caches: each load has half of its lines)
+  __device__ __forceinline__ Raw load(size_t at) const {
+    return Raw{*(const f32x4*)(p + at), *(const f32x4*)(p + at + 4)};
+  }
+  static __device__ __forceinline__ void values(const Raw& r, float* v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = r.a[i];
+      v[4 + i] = r.b[i];
+    }
+  }
+};
+
+// The root mean square norm that keeps its input: y is that of norm_kernel, bit
+// for bit (the same threads hold the same values and join their sums in the
+// same order), and a row's pieces of 4 neighbouring threads are a block of 32.
+// A block goes over several rows with the weight in registers and, up to 16384
+// values, the next row in flight: taken from L2 for every row, the weight's 4
+// bytes a value were as much as x, y and the codes together (8192 x 6144 bf16:
+// 47 us so, 42 now).
+template <typename T, typename U, int P>
+__global__ __launch_bounds__(kMaxThreads) void norm_checkpoint_kernel(
+    Eight<T> x, const float* __restrict__ w, float eps, int rows, int H, U* y,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr bool kAhead = P <= 2;
+  __shared__ float part[4][kMaxWaves];
+  const bool one_wave = blockDim.x == kWave;
+  const long long step = (long long)gridDim.x * blockDim.y;
+  long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const Pieces<P, 8> pieces(H);
+  typename Eight<T>::Raw next[P];
+  const auto fetch = [&](long long row) {
+    const size_t start = (size_t)min(row, (long long)rows - 1) * H;
+#pragma unroll
+    for (int p = 0; p < P; ++p) next[p] = x.load(start + pieces.at[p]);
+  };
+  if (kAhead) fetch(t);
+  float g[P][8];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[p][i] = 1.0f;
+    if (w) Row8<float>::load(w + pieces.at[p], g[p]);
+  }
+  const auto arrived = [&]() {
+#pragma unroll
+    for (int p = 0; p < P; ++p) Eight<T>::arrived(next[p]);
+  };
+  if (kAhead) arrived();
+  int turn = 0;   // the sums of one row are read while those of the next are written
+  for (; t < rows; t += step, turn ^= 2) {
+    const size_t row = (size_t)t * H;
+    float v[P][8];
+    float ss = 0.0f;
+    if (!kAhead) fetch(t);
+#pragma unroll
+    for (int p = 0; p < P; ++p) Eight<T>::values(next[p], v[p]);
+    if (kAhead) fetch(t + step);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      unsigned byte;
+      const mx8::Codes<8> c = mx8::encode<8>(v[p], byte);
+      if (pieces.inside(p)) {
+        const size_t at = row + pieces.at[p];
+        *(mx8::Codes<8>*)(codes + at) = c;
+        if ((threadIdx.x & 3) == 0) scales[at / 32] = (uint8_t)byte;
+      }
+    }
+    pieces.clear_behind(v);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v[p][i], v[p][i], ss);
+    const float r = inv_rms(v, ss, eps, H, part + turn, one_wave);
+    // the next row's loads end here, so that nothing waits for this row's stores
+    if (kAhead) arrived();
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = v[p][i] * r * g[p][i];
+      // past the caches, which then have the codes for the backward pass (113 -> 110 us
+      // both ways, 8192 x 6144); fp32 in pieces of 8 would be half lines
+      if (pieces.inside(p)) {
+        if constexpr (std::is_same<U, bf16>::value)
+          store_past<8>(y + row + pieces.at[p], v[p]);
+        else
+          Row8<U>::store(y + row + pieces.at[p], v[p]);
+      }
+    }
+  }
+}
 
 // v = v - mean(v).
 template <int WAVES, int P, int VEC>
@@ -167,76 +227,103 @@ template <int P, int VEC> __device__ __forceinline__ void scale(float (&v)[P][VE
 }
 
 // SAVE: x in 8 bits to codes and scales too; the pieces of 32 / VEC neighbouring
-// threads are a block.
+// threads are a block.  A block goes over the rows blockIdx.x * blockDim.y +
+// threadIdx.y, and so on; up to 12288 values its threads have weight and bias in
+// registers and the next row in flight.  (From L2 for every row, the two were
+// more than x and y together: 8192 x 6144 fp32 to bf16 55.7 us so, 48.6 now.)
 template <typename T, typename U, int P, int VEC, int THREADS, bool SAVE>
 __global__ __launch_bounds__(THREADS) void layer_norm_kernel(
     Source<T, VEC> x, const float* __restrict__ w, const float* __restrict__ b, float eps,
     int rows, int H, U* y, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr bool kAhead = THREADS <= 512;
   constexpr int kWaves = THREADS <= 256 ? 4 : 16;
   __shared__ __attribute__((aligned(16))) float part[4][kWaves];
-  if (blockDim.y == 1) {
-    if (threadIdx.x < 4 * kWaves) (&part[0][0])[threadIdx.x] = 0.0f;
-    lds_barrier();
-  }
-  const unsigned t = row_of_thread();
-  if (t >= (unsigned)rows) return;   // a whole wave, and then blocks have no barrier
-  const size_t row = (size_t)t * H;
+  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 4 * kWaves;
+       i += blockDim.x * blockDim.y)
+    (&part[0][0])[i] = 0.0f;
+  __syncthreads();
+  const long long step = (long long)gridDim.x * blockDim.y;
+  long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   const Pieces<P, VEC> pieces(H);
   const float inv_h = 1.0f / (float)H;
-  float v[P][VEC];
-  const auto load = [&]() {
-    typename Source<T, VEC>::Raw raw[P];
+  typedef typename Source<T, VEC>::Raw Raw;
+  Raw next[P];
+  // (the last row where there is no next one)
+  const auto fetch = [&](long long row) {
+    const size_t start = (size_t)min(row, (long long)rows - 1) * H;
 #pragma unroll
-    for (int p = 0; p < P; ++p) raw[p] = x.load(row + pieces.at[p]);
-#pragma unroll
-    for (int p = 0; p < P; ++p) Source<T, VEC>::values(raw[p], v[p]);
+    for (int p = 0; p < P; ++p) next[p] = x.load(start + pieces.at[p]);
   };
-  load();
-  if (SAVE) {
+  if (kAhead) fetch(t);
+  float weight[kAhead ? P : 1][VEC], bias[kAhead ? P : 1][VEC];
+  const auto affine = [&](int p, float* g, float* c) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      unsigned byte;
-      const mx8::Codes<VEC> c = mx8::encode<VEC>(v[p], byte);
-      if (pieces.inside(p)) {   // all lanes of a block or none
-        const size_t at = row + pieces.at[p];
-        __builtin_nontemporal_store(c, (mx8::Codes<VEC>*)(codes + at));
-        if (pieces.at[p] % 32 == 0) scales[at / 32] = (uint8_t)byte;
+    for (int i = 0; i < VEC; ++i) {
+      g[i] = 1.0f;
+      c[i] = 0.0f;
+    }
+    if (w) load_floats<VEC>(w + pieces.at[p], g);
+    if (b) load_floats<VEC>(b + pieces.at[p], c);
+  };
+  if (kAhead) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) affine(p, weight[p], bias[p]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) Source<T, VEC>::arrived(next[p]);
+  }
+  for (; t < rows; t += step) {
+    const size_t row = (size_t)t * H;
+    float v[P][VEC];
+    if (!kAhead) fetch(t);
+#pragma unroll
+    for (int p = 0; p < P; ++p) Source<T, VEC>::values(next[p], v[p]);
+    if (kAhead) fetch(t + step);
+    if (SAVE) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        unsigned byte;
+        const mx8::Codes<VEC> c = mx8::encode<VEC>(v[p], byte);
+        if (pieces.inside(p)) {   // all lanes of a block or none
+          const size_t at = row + pieces.at[p];
+          *(mx8::Codes<VEC>*)(codes + at) = c;
+          if (pieces.at[p] % 32 == 0) scales[at / 32] = (uint8_t)byte;
+        }
       }
     }
-  }
-  pieces.clear_behind(v);
-  center(v, pieces, H, part);
-  float ss = squares(v, part + 1), f = 1.0f;
-  if (too_large(ss)) {
-    f = 0x1p-96f;
-    load();   // the deviations may be lost already
     pieces.clear_behind(v);
-    scale(v, f);
-    center(v, pieces, H, part + 2);
-    ss = squares(v, part + 3);
-  } else if (too_small(ss, eps)) {
-    f = 0x1p96f;
-    scale(v, f);
-    ss = squares(v, part + 2);
-  }
-  const float r = rsqrtf(ss * inv_h + eps * f * f);
+    center(v, pieces, H, part);
+    float ss = squares(v, part + 1), f = 1.0f;
+    if (too_large(ss)) {
+      f = 0x1p-96f;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    float g[VEC];
-    if (w) {
-      load_floats<VEC>(w + pieces.at[p], g);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[p][i] = v[p][i] * r * g[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[p][i] *= r;
+      for (int p = 0; p < P; ++p) {   // the deviations may be lost already
+        const Raw again = x.load(row + pieces.at[p]);
+        Source<T, VEC>::values(again, v[p]);
+      }
+      pieces.clear_behind(v);
+      scale(v, f);
+      center(v, pieces, H, part + 2);
+      ss = squares(v, part + 3);
+    } else if (too_small(ss, eps)) {
+      f = 0x1p96f;
+      scale(v, f);
+      ss = squares(v, part + 2);
     }
-    if (b) {
-      load_floats<VEC>(b + pieces.at[p], g);
+    const float r = rsqrtf(ss * inv_h + eps * f * f);
+    // the next row's loads end here, so that nothing waits for this row's stores
+    if (kAhead) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[p][i] += g[i];
+      for (int p = 0; p < P; ++p) Source<T, VEC>::arrived(next[p]);
     }
-    if (pieces.inside(p)) store_past<VEC>(y + row + pieces.at[p], v[p]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float g[VEC], c[VEC];
+      if (!kAhead) affine(p, g, c);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        v[p][i] = fmaf(v[p][i] * r, kAhead ? weight[p][i] : g[i], kAhead ? bias[p][i] : c[i]);
+      if (pieces.inside(p)) store_past<VEC>(y + row + pieces.at[p], v[p]);
+    }
   }
 }
 
@@ -464,32 +551,47 @@ __global__ __launch_bounds__(kWave* kJoinWaves) void join_sums(const float* __re
   out[h] = v;
 }
 
+// Blocks that go over rows, per_cu of them a CU but for no more than 32 waves.
+void bound_blocks(Shape& s, int T, unsigned per_cu) {
+  const unsigned most = 32 * kWave / (s.block.x * s.block.y);
+  s.grid = dim3(std::min(ceil_div(T, s.block.y), 256 * std::max(1u, std::min(per_cu, most))));
+}
 // Threads of a row, P pieces of 8 values each: up to 6144 values at most 256
 // threads, four rows of a wave to a block where that is enough for one; up to
-// 12288 at most 512.
-// (P - 1) * 8 values for every thread lie inside the row: Pieces counts on it.
-Shape row_shape(int T, int H) {
+// 12288 at most 512.  (P - 1) * 8 values for every thread lie inside the row:
+// Pieces counts on it.
+Shape row_shape(int H) {
   Shape s;
   s.P = H <= 6144 ? ceil_div(H, 2048) : H <= 12288 ? ceil_div(H, 4096) : 4;
   const int per = ceil_div(ceil_div(H, 8 * s.P), kWave) * kWave;
   s.block = dim3(per, per == kWave ? 4 : 1);
-  const unsigned blocks = ceil_div(T, s.block.y);
-  s.grid.x = std::min(blocks, kMaxGridX);
-  s.grid.y = ceil_div(blocks, s.grid.x);
   return s;
 }
-// The backward pass's blocks: for two waves a SIMD, each with a few rows.
-Shape backward_shape(int T, int H) {
-  Shape s = row_shape(T, H);
-  const unsigned most = 256 * std::max(1u, 512 / (s.block.x * s.block.y));
-  s.grid = dim3(std::min(ceil_div(T, s.block.y), most));
+// The forward pass: as many blocks as have up to 32 KB of rows at a time (with
+// the next ones in flight as much again).  More of them read and write in more
+// places at once and are slower, fewer leave the memory idle: 8192 x 6144 fp32
+// 49 us with one block of 24 KB, 51 with four; 16384 x 2048 51 with one of 8 KB, 34
+// with four.
+Shape forward_shape(int T, int H, int x_bytes) {
+  Shape s = row_shape(H);
+  bound_blocks(s, T, 32768 / (H * x_bytes * s.block.y));
   return s;
 }
+// The backward pass: as few blocks as have 20 KB of loads at a time, for the same
+// reason (8192 x 6144 with fp32 rows 121 us with one block, 129 with two; 16384 x
+// 2048 bf16 68 with one of 12 KB, 53 with two, 55 with three), and each block's
+// sums are written and read again.  bytes: of a value in all that is read.
+Shape backward_shape(int T, int H, int bytes) {
+  Shape s = row_shape(H);
+  bound_blocks(s, T, ceil_div(20480, H * bytes * s.block.y));
+  return s;
+}
+constexpr int kLeastBytes = 4;   // dy and x of 16 bits, no residual
 
 }  // namespace
 
 size_t norm_backward_ws_bytes(int T, int H) {
-  return (size_t)backward_shape(T, H).grid.x * 2 * H * sizeof(float);
+  return (size_t)backward_shape(T, H, kLeastBytes).grid.x * 2 * H * sizeof(float);
 }
 
 namespace {
@@ -515,11 +617,12 @@ namespace {
 template <typename T, typename U>
 void checkpoint_t(const void* x, const float* w, float eps, int T_, int H, void* y,
                   uint8_t* codes, uint8_t* scales, hipStream_t st) {
-  const Shape s = shape(T_, H);
+  Shape s = shape(T_, H);
+  bound_blocks(s, T_, std::max(2u, 32768u / (H * (unsigned)sizeof(T) * s.block.y)));
 #define MOE_NORM(P)                                                                       \
   MOE_LAUNCH("norm_checkpoint", st,                                                       \
              norm_checkpoint_kernel<T, U, P><<<s.grid, s.block, 0, st>>>(                 \
-                 (const T*)x, w, eps, T_, H, (U*)y, codes, scales))
+                 Eight<T>{(const T*)x}, w, eps, T_, H, (U*)y, codes, scales))
   if (s.P == 1)
     MOE_NORM(1);
   else if (s.P == 2)
@@ -532,7 +635,7 @@ void checkpoint_t(const void* x, const float* w, float eps, int T_, int H, void*
 template <typename T, typename U>
 void layer_norm_t(const void* x, const float* w, const float* b, float eps, int T_, int H,
                   void* y, uint8_t* codes, uint8_t* scales, hipStream_t st) {
-  const Shape s = row_shape(T_, H);
+  const Shape s = forward_shape(T_, H, sizeof(T));
   constexpr int VEC = piece_of<T, U>();
 #define MOE_NORM(P, THREADS, SAVE)                                                            \
   MOE_LAUNCH("layer_norm", st,                                                                \
@@ -563,7 +666,9 @@ template <typename DY, typename X, typename DX>
 void backward_t(bool mean, const void* dy, const void* x, const uint8_t* x_scales, const float* w,
                 float eps, int T, int H, const void* d_residual, void* dx, float* d_weight,
                 float* d_bias, float* ws, hipStream_t st) {
-  const Shape s = backward_shape(T, H);
+  // (8-bit rows count as the bf16 ones that hold the same: their sums are the same bits)
+  constexpr int kX = std::is_same<X, float>::value ? 4 : 2;
+  const Shape s = backward_shape(T, H, (int)sizeof(DY) + kX + (d_residual ? (int)sizeof(DX) : 0));
   constexpr int VEC = piece_of<DY, X, DX>();
   // one block has the whole sums
   const bool join = s.grid.x > 1 && (d_weight || d_bias);
