@@ -19,7 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCountThreads = 1024;   // at least kMaxRouteE: an expert a thread
 constexpr int kLossThreads = 1024;
-constexpr unsigned kLossBlocks = 256, kGradientBlocks = 4096;
+constexpr unsigned kLossBlocks = 256, kGradientBlocks = 2048;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // Sequence of a token, or -1 for padding.
@@ -126,44 +126,51 @@ __global__ __launch_bounds__(kThreads) void balance_clear(int32_t* counts, long 
   if (i == 0) *ticket = 0;
 }
 
-// A block counts the picks of kCountTokens tokens: those of the first one's
-// sequence, as a rule all of them, in LDS, the others in memory.
+// A block counts the picks of kCountTokens tokens at a time: those of the first
+// one's sequence, as a rule all of them, in LDS, the others in memory.
 constexpr int kCountTokens = 256;
+constexpr unsigned kCountBlocks = 4096;
 __global__ __launch_bounds__(kCountThreads) void balance_count(
     const int32_t* __restrict__ idx, const int32_t* __restrict__ seq, int n_seq, int T, int E,
     int K, int32_t* __restrict__ counts, int32_t* __restrict__ tokens) {
   __shared__ int hist[kMaxRouteE];
   __shared__ int mine, all;
-  const int t0 = blockIdx.x * kCountTokens, n = min(kCountTokens, T - t0);
-  const int home = sequence(seq, n_seq, t0);
-  for (int e = threadIdx.x; e < E; e += kCountThreads) hist[e] = 0;
-  if (threadIdx.x == 0) mine = all = 0;
-  __syncthreads();
+  for (long long t0 = (long long)blockIdx.x * kCountTokens; t0 < T;
+       t0 += (long long)gridDim.x * kCountTokens) {
+    const int n = (int)min((long long)kCountTokens, T - t0);
+    const int home = sequence(seq, n_seq, t0);
+    for (int e = threadIdx.x; e < E; e += kCountThreads) hist[e] = 0;
+    if (threadIdx.x == 0) mine = all = 0;
+    __syncthreads();
 #pragma unroll 4
-  for (int i = threadIdx.x; i < n * K; i += kCountThreads) {
-    const int e = idx[(size_t)t0 * K + i], s = sequence(seq, n_seq, t0 + i / K);
-    if (e < 0 || e >= E || s < 0) continue;
-    if (s == home)
-      atomicAdd(&hist[e], 1);
-    else
-      atomicAdd(&counts[(size_t)s * E + e], 1);
-  }
-  if (threadIdx.x < n) {
-    const int s = sequence(seq, n_seq, t0 + threadIdx.x);
-    if (s >= 0) {
-      atomicAdd(&all, 1);
+    for (int i = threadIdx.x; i < n * K; i += kCountThreads) {
+      const int e = idx[t0 * K + i], s = sequence(seq, n_seq, t0 + i / K);
+      if (e < 0 || e >= E || s < 0) continue;
       if (s == home)
-        atomicAdd(&mine, 1);
+        atomicAdd(&hist[e], 1);
       else
-        atomicAdd(&tokens[s], 1);
+        atomicAdd(&counts[(size_t)s * E + e], 1);
     }
+    if (threadIdx.x < n) {
+      const int s = sequence(seq, n_seq, t0 + threadIdx.x);
+      if (s >= 0) {
+        atomicAdd(&all, 1);
+        if (s == home)
+          atomicAdd(&mine, 1);
+        else
+          atomicAdd(&tokens[s], 1);
+      }
+    }
+    __syncthreads();
+    if (home >= 0)
+      for (int e = threadIdx.x; e < E; e += kCountThreads)
+        if (hist[e]) atomicAdd(&counts[(size_t)home * E + e], hist[e]);
+    if (threadIdx.x == 0) {
+      if (all) atomicAdd(&tokens[n_seq], all);
+      if (mine) atomicAdd(&tokens[home], mine);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (threadIdx.x == 0 && all) atomicAdd(&tokens[n_seq], all);
-  if (home < 0) return;
-  for (int e = threadIdx.x; e < E; e += kCountThreads)
-    if (hist[e]) atomicAdd(&counts[(size_t)home * E + e], hist[e]);
-  if (threadIdx.x == 0 && mine) atomicAdd(&tokens[home], mine);
 }
 
 __global__ __launch_bounds__(kCountThreads) void balance_load(const int32_t* __restrict__ counts,
@@ -465,7 +472,7 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const in
                balance_clear<<<ceil_div(n, kThreads), kThreads, 0, s>>>(
                    counts, (long long)n_seq * E, tokens, n_seq + 1, ticket));
     MOE_LAUNCH("balance_count", s,
-               balance_count<<<ceil_div(T, kCountTokens), kCountThreads, 0, s>>>(
+               balance_count<<<std::min(ceil_div(T, kCountTokens), kCountBlocks), kCountThreads, 0, s>>>(
                    idx, seq, n_seq, T, E, K, counts, tokens));
     MOE_LAUNCH("balance_load", s,
                balance_load<<<n_seq, kCountThreads, 0, s>>>(counts, tokens, group, E, K, load));

@@ -207,3 +207,49 @@ def test_more_tokens_than_blocks_at_a_time():
     part = np.r_[0:50, 8190:8210, 65530:65545, 69980:70001]
     want, e = ref.route_backward(logits[part].astype(np.float64), idx[part], d_gate[part].astype(np.float64))
     ref.close(d[_t(part, torch.long)], want, e + 1e-37)
+
+
+@pytest.mark.parametrize("E", [24, 96, 768])
+def test_tensors_that_start_anywhere(E):
+    """Logits, loads and gradients aligned to 4 bytes alone."""
+    T, K, n = 200, 4, 3
+    logits, idx, seq = _case(T, E, K, n)
+    d_gate = np.random.default_rng(1).standard_normal((T, K)).astype(np.float32)
+
+    def at(a, dtype, off):
+        flat = torch.empty(a.size + 8, dtype=dtype, device=device())
+        v = flat[off:off + a.size].view(a.shape)
+        v.copy_(_t(a, dtype))
+        return v
+
+    outs = []
+    for off in (0, 1, 3):
+        x, i, g = at(logits, F32, off), at(idx, I32, off), at(d_gate, F32, off)
+        s = at(seq, I32, off)
+        got = _loss(x, i, s, n)
+        load, d = at(got["load"].cpu().numpy(), F32, off), at(np.zeros((T, E), np.float32), F32, off)
+        moe.moe_route_backward(x, d, i, g, got["tokens"], load, s, None, 0.02, 0.003)
+        outs.append((got, d.clone()))
+    want, e = ref.route_backward(logits.astype(np.float64), idx, d_gate.astype(np.float64), seq, n,
+                                 outs[0][0]["tokens"].cpu().numpy(), ref.f64(outs[0][0]["load"]), None,
+                                 float(np.float32(0.02)), float(np.float32(0.003)))
+    losses, e_l, *_ = ref.balance_loss(logits.astype(np.float64), idx, seq, n, None, 0.02, 0.003)
+    for got, d in outs:
+        for k in ("counts", "tokens", "load"):
+            assert torch.equal(got[k], outs[0][0][k]), k
+        ref.close(got["losses"], losses, e_l)
+        ref.close(d, want, e + 1e-37)
+
+
+def test_more_tokens_than_a_launch_has_threads():
+    """2^30 tokens and more of a pool of one expert: every probability is 1, every load 1."""
+    T = (1 << 30) + 777
+    logits = torch.full((T, 1), 0.5, device=device())
+    idx = torch.zeros((T, 1), dtype=I32, device=device())
+    got = _loss(logits, idx, None, 1, None, 0.25, 2.0)
+    assert got["counts"].tolist() == [[T]] and got["tokens"].tolist() == [T, T]
+    assert got["load"].tolist() == [[1.0]] and got["losses"].tolist() == [0.25, 0.5]
+    idx.view(F32).fill_(1.0)                         # the picks' memory as the gates' gradient
+    picks = torch.zeros((T, 1), dtype=I32, device=device())
+    moe.moe_route_backward(logits, logits, picks, idx.view(F32), got["tokens"], got["load"], None, None, 0.25, 0.0)
+    assert (logits == 0).all()

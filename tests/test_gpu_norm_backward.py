@@ -215,3 +215,31 @@ def test_weight_gradient_alone_or_bias_gradient_alone():
     for one in (dict(d_weight=_nan((H,), F32)), dict(d_bias=_nan((H,), F32))):
         moe.moe_layer_norm_backward(dy, x, w, _nan((T, H), F32), ws=ws, eps=EPS, **one)
         assert torch.equal(list(one.values())[0], want[1] if "d_weight" in one else want[2])
+
+
+@pytest.mark.parametrize("T,H", [((1 << 28) + 13, 8), ((1 << 25) + 3, 520)])
+def test_very_many_rows(T, H):
+    """Rows past 2^32 values: the ends against the same rows by themselves, the bias's gradient a count."""
+    x = torch.empty((T, H), dtype=BF16, device=device())
+    ends = torch.cat([torch.arange(40), torch.arange(T - 40, T)]).to(device())
+    part = _x(80, H, BF16)
+    x.fill_(0.5)
+    x[ends] = part
+    y = torch.empty_like(x)
+    w, b = _weights(H)
+    moe.moe_layer_norm(x, w, b, y, EPS)
+    few = _nan((80, H), BF16)
+    moe.moe_layer_norm(part, w, b, few, EPS)
+    assert torch.equal(y[ends], few)
+    assert torch.equal(y[T // 2], b.to(BF16))        # a constant row: the bias
+    y.fill_(0)
+    dy = _x(80, H, BF16, 3)
+    y[ends] = dy
+    dw, db = _nan((H,), F32), _nan((H,), F32)
+    ws = torch.empty(moe.moe_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=device())
+    moe.moe_layer_norm_backward(y, x, w, x, dw, db, ws, EPS)      # in place of x
+    want = _backward(dy, part, w, _nan((80, H), BF16), True)
+    assert torch.equal(x[ends], want[0]) and (x[T // 2] == 0).all()
+    (_, dw64, db64), (_, e_w, e_b) = ref.norm_backward(ref.f64(dy), ref.f64(part), ref.f64(w), EPS, True)
+    ref.close(dw, dw64, ref.rounded(dw64, e_w, F32))              # (zeros in between add nothing)
+    ref.close(db, db64, ref.rounded(db64, e_b, F32))
