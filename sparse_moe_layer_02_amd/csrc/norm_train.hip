@@ -668,7 +668,12 @@ void backward_t(bool mean, const void* dy, const void* x, const uint8_t* x_scale
                 float* d_bias, float* ws, hipStream_t st) {
   // (8-bit rows count as the bf16 ones that hold the same: their sums are the same bits)
   constexpr int kX = std::is_same<X, float>::value ? 4 : 2;
-  const Shape s = backward_shape(T, H, (int)sizeof(DY) + kX + (d_residual ? (int)sizeof(DX) : 0));
+  Shape s = backward_shape(T, H, (int)sizeof(DY) + kX + (d_residual ? (int)sizeof(DX) : 0));
+  // A few rows are one block's, which has the whole sums: 8.2 us a call for 4 to 16
+  // rows of 256 and 1 to 4 of 2048 values, with a launch that joins the sums of
+  // more blocks 10.7 to 11.0.  On the GPU alone the fifth row in turn (of 6144
+  // values the third) takes longer than that launch.
+  if ((d_weight || d_bias) && s.grid.x <= (H <= 4096 ? 4 : 2)) s.grid.x = 1;
   constexpr int VEC = piece_of<DY, X, DX>();
   // one block has the whole sums
   const bool join = s.grid.x > 1 && (d_weight || d_bias);
