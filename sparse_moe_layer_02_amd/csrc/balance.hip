@@ -449,10 +449,7 @@ constexpr long long kSequencePicks = 32768, kSequenceTokens = 1 << 20;
 
 }  // namespace
 
-size_t balance_ws_bytes(int T, int E, int n_seq) {
-  (void)E;
-  (void)n_seq;
-  (void)T;
+size_t balance_ws_bytes() {
   return kTicketBytes + kLossBlocks * 2 * sizeof(double);
 }
 

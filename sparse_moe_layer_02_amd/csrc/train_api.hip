@@ -57,7 +57,7 @@ extern "C" {
 
 size_t moe_balance_loss_workspace_bytes(int T, int E, int n_seq) {
   if (T < 1 || E < 1 || E > kMaxRouteE || n_seq < 1 || n_seq > kMaxSeq) return 0;
-  return balance_ws_bytes(T, E, n_seq);
+  return balance_ws_bytes();
 }
 
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const int32_t* seq,
@@ -71,7 +71,7 @@ moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const 
       !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(load, 4) || !aligned(losses, 4) ||
       !aligned(ws, 256))
     return MOE_ERR_ALIGN;
-  if (ws_bytes < balance_ws_bytes(T, E, n_seq)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < balance_ws_bytes()) return MOE_ERR_WORKSPACE;
   return launched(launch_balance_loss(logits, topk_idx, seq, n_seq, group, T, E, K, balance_coef,
                                       z_coef, counts, tokens, load, losses, ws,
                                       (hipStream_t)stream));

@@ -9,7 +9,7 @@ namespace moe {
 
 constexpr int kMaxRouteE = 1024;   // a wave's row: up to 16 logits a lane
 
-size_t balance_ws_bytes(int T, int E, int n_seq);
+size_t balance_ws_bytes();
 hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* seq,
                                int n_seq, const int32_t* group, int T, int E, int K,
                                float balance_coef, float z_coef, int32_t* counts, int32_t* tokens,
