@@ -56,23 +56,22 @@ __device__ __forceinline__ void loads_of(int s, int picks, int g, bool grouped, 
   load[(size_t)s * E + e] = v;
 }
 
-// Counts and loads in one launch: block s looks at all tokens' sequences, 64
-// tokens to a wave, and counts the picks of those of sequence s in LDS.
+// Counts and loads of sequence s by a block, which looks at all tokens'
+// sequences, 64 tokens to a wave, and counts the picks of those of its own in LDS.
 constexpr int kLook = 16;   // windows of 64 tokens whose sequences a wave has in flight
 constexpr int kPicks = 12;  // picks that a lane has in flight
-__global__ __launch_bounds__(kCountThreads) void balance_count_sequence(
-    const int32_t* __restrict__ idx, const int32_t* __restrict__ seq, int n_seq,
-    const int32_t* __restrict__ group, int T, int E, int K, int32_t* __restrict__ counts,
-    int32_t* __restrict__ tokens, float* __restrict__ load, unsigned* __restrict__ ticket) {
-  __shared__ int hist[kMaxRouteE], sum[kMaxRouteE], size[kMaxRouteE];
-  __shared__ int mine, all;
-  const int s = blockIdx.x, lane = threadIdx.x & (kWave - 1), expert = threadIdx.x;
+struct CountLds {
+  int hist[kMaxRouteE], sum[kMaxRouteE], size[kMaxRouteE];
+  int mine, all;
+};
+__device__ __forceinline__ void count_sequence(int s, CountLds& lds, const int32_t* idx,
+                                               const int32_t* seq, int n_seq,
+                                               const int32_t* group, int T, int E, int K,
+                                               int32_t* counts, int32_t* tokens, float* load) {
+  const int lane = threadIdx.x & (kWave - 1), expert = threadIdx.x;
   const int g = group && expert < E ? group[expert] : expert;
-  hist[expert] = 0;
-  if (threadIdx.x == 0) {
-    mine = all = 0;
-    if (s == 0) *ticket = 0;
-  }
+  lds.hist[expert] = 0;
+  if (threadIdx.x == 0) lds.mine = lds.all = 0;
   __syncthreads();
   int n = 0, inside = 0;
   for (int t0 = threadIdx.x / kWave * kWave; t0 < T; t0 += kLook * kCountThreads) {
@@ -100,21 +99,30 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_sequence(
         }
 #pragma unroll
         for (int k = 0; k < kPicks; ++k)
-          if (e[k] >= 0 && e[k] < E) atomicAdd(&hist[e[k]], 1);
+          if (e[k] >= 0 && e[k] < E) atomicAdd(&lds.hist[e[k]], 1);
       }
     }
   }
   if (lane == 0) {
-    atomicAdd(&mine, n);
-    atomicAdd(&all, inside);
+    atomicAdd(&lds.mine, n);
+    atomicAdd(&lds.all, inside);
   }
   __syncthreads();
-  if (expert < E) counts[(size_t)s * E + expert] = hist[expert];
+  if (expert < E) counts[(size_t)s * E + expert] = lds.hist[expert];
   if (threadIdx.x == 0) {
-    tokens[s] = mine;
-    if (s == 0) tokens[n_seq] = all;
+    tokens[s] = lds.mine;
+    if (s == 0) tokens[n_seq] = lds.all;
   }
-  loads_of(s, hist[expert], g, group != nullptr, mine, E, K, sum, size, load);
+  loads_of(s, lds.hist[expert], g, group != nullptr, lds.mine, E, K, lds.sum, lds.size, load);
+}
+
+__global__ __launch_bounds__(kCountThreads) void balance_count_sequence(
+    const int32_t* __restrict__ idx, const int32_t* __restrict__ seq, int n_seq,
+    const int32_t* __restrict__ group, int T, int E, int K, int32_t* __restrict__ counts,
+    int32_t* __restrict__ tokens, float* __restrict__ load, unsigned* __restrict__ ticket) {
+  __shared__ CountLds lds;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
+  count_sequence(blockIdx.x, lds, idx, seq, n_seq, group, T, E, K, counts, tokens, load);
 }
 
 __global__ __launch_bounds__(kThreads) void balance_clear(int32_t* counts, long long n,
@@ -248,26 +256,16 @@ struct RowOf {
   }
 };
 
-// Sums over the rows of load p and of lse^2, a block's to `sums`, and from those
-// the losses, by the block that is the last to have written its own.  What the
-// blocks hand each other passes the caches that they do not share (accesses of
-// agent scope), and a block's sums have arrived (vmcnt 0) before its ticket is
-// drawn: a fence would write back a whole L2 for them, 30 us for 1024 blocks.
-// A ticket costs 7 ns, so the blocks are few and large.
+// Sums of load p and of lse^2 over the rows first, first + step, ..., in the
+// first lanes of the rows' groups.
 template <int W, int N, int VEC>
-__global__ __launch_bounds__(kLossThreads) void balance_rows(
-    const float* __restrict__ logits, const int32_t* __restrict__ seq, int n_seq, int T, int E,
-    const float* __restrict__ load, const int32_t* __restrict__ tokens, float balance_coef,
-    float z_coef, double* sums, unsigned* ticket, float* __restrict__ losses) {
+__device__ __forceinline__ void loss_rows(const float* logits, const int32_t* seq, int n_seq,
+                                          int T, int E, const float* load, long long first,
+                                          long long step, double (&v)[2]) {
   typedef RowOf<W, N, VEC> Row;
-  constexpr int kRows = kLossThreads / W, kWaves = kLossThreads / kWave;
-  __shared__ double part[2][kWaves];
-  __shared__ bool last;
-  const int l = threadIdx.x % W, row = threadIdx.x / W;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  double v[2] = {0.0, 0.0};   // in a group's first lane
-  for (long long t = (long long)blockIdx.x * kRows + row; t < T;
-       t += (long long)gridDim.x * kRows) {
+  const int l = threadIdx.x % W;
+  v[0] = v[1] = 0.0;
+  for (long long t = first; t < T; t += step) {
     const int s = sequence(seq, n_seq, t);
     if (s < 0) continue;
     float p[N][VEC], f[N][VEC];
@@ -285,22 +283,51 @@ __global__ __launch_bounds__(kLossThreads) void balance_rows(
       v[1] += (double)lse * lse;
     }
   }
-  // the waves' sums, then the block's, in thread 0
-  const auto join = [&]() {
+}
+
+// The waves' sums, then the block's, in thread 0.
+__device__ __forceinline__ void join_losses(double (&v)[2], double (*part)[kLossThreads / kWave]) {
+  constexpr int kWaves = kLossThreads / kWave;
 #pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int off = kWave / 2; off > 0; off >>= 1) v[k] += __shfl_xor(v[k], off);
+    if ((threadIdx.x & (kWave - 1)) == 0) part[k][threadIdx.x / kWave] = v[k];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
     for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int off = kWave / 2; off > 0; off >>= 1) v[k] += __shfl_xor(v[k], off);
-      if (lane == 0) part[k][wave] = v[k];
+      v[k] = 0.0;
+      for (int w = 0; w < kWaves; ++w) v[k] += part[k][w];
     }
-    __syncthreads();
-    if (threadIdx.x == 0)
-      for (int k = 0; k < 2; ++k) {
-        v[k] = 0.0;
-        for (int w = 0; w < kWaves; ++w) v[k] += part[k][w];
-      }
-  };
-  join();
+}
+
+__device__ __forceinline__ void write_losses(const double (&v)[2], int all, float balance_coef,
+                                             float z_coef, float* losses) {
+  losses[0] = all > 0 ? (float)(balance_coef * v[0] / all) : 0.0f;
+  losses[1] = all > 0 ? (float)(z_coef * v[1] / all) : 0.0f;
+}
+
+// The sweep over the logits: a block's sums go to `sums`, and the block that is
+// the last to have written its own takes the losses from all.  What the
+// blocks hand each other passes the caches that they do not share (accesses of
+// agent scope), and a block's sums have arrived (vmcnt 0) before its ticket is
+// drawn: a fence would write back a whole L2 for them, 30 us for 1024 blocks.
+// A ticket costs 7 ns, so the blocks are few and large.  (16384 x 768: 13 us, 3.8
+// TB/s, some of it from the last cache.)
+template <int W, int N, int VEC>
+__global__ __launch_bounds__(kLossThreads) void balance_rows(
+    const float* __restrict__ logits, const int32_t* __restrict__ seq, int n_seq, int T, int E,
+    const float* __restrict__ load, const int32_t* __restrict__ tokens, float balance_coef,
+    float z_coef, double* sums, unsigned* ticket, float* __restrict__ losses) {
+  constexpr int kRows = kLossThreads / W;
+  __shared__ double part[2][kLossThreads / kWave];
+  __shared__ bool last;
+  double v[2];
+  loss_rows<W, N, VEC>(logits, seq, n_seq, T, E, load,
+                       (long long)blockIdx.x * kRows + threadIdx.x / W,
+                       (long long)gridDim.x * kRows, v);
+  join_losses(v, part);
   if (threadIdx.x == 0) {
     for (int k = 0; k < 2; ++k)
       __hip_atomic_store(&sums[2 * blockIdx.x + k], v[k], __ATOMIC_RELAXED,
@@ -318,12 +345,26 @@ __global__ __launch_bounds__(kLossThreads) void balance_rows(
                ? __hip_atomic_load(&sums[2 * threadIdx.x + k], __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT)
                : 0.0;
-  join();
-  if (threadIdx.x == 0) {
-    const int all = tokens[n_seq];
-    losses[0] = all > 0 ? (float)(balance_coef * v[0] / all) : 0.0f;
-    losses[1] = all > 0 ? (float)(z_coef * v[1] / all) : 0.0f;
-  }
+  join_losses(v, part);
+  if (threadIdx.x == 0) write_losses(v, tokens[n_seq], balance_coef, z_coef, losses);
+}
+
+// All of it by one block, for one sequence of few rows.
+template <int W, int N, int VEC>
+__global__ __launch_bounds__(kLossThreads) void balance_alone(
+    const float* __restrict__ logits, const int32_t* __restrict__ idx,
+    const int32_t* __restrict__ seq, const int32_t* __restrict__ group, int T, int E, int K,
+    float balance_coef, float z_coef, int32_t* counts, int32_t* tokens, float* load,
+    float* __restrict__ losses) {
+  static_assert(kLossThreads == kCountThreads, "one block counts and sums");
+  __shared__ CountLds lds;
+  __shared__ double part[2][kLossThreads / kWave];
+  count_sequence(0, lds, idx, seq, 1, group, T, E, K, counts, tokens, load);
+  __syncthreads();   // the loads that this block has written, to all of it
+  double v[2];
+  loss_rows<W, N, VEC>(logits, seq, 1, T, E, load, threadIdx.x / W, kLossThreads / W, v);
+  join_losses(v, part);
+  if (threadIdx.x == 0) write_losses(v, lds.all, balance_coef, z_coef, losses);
 }
 
 // d_logits may be logits: a group has read the row that it overwrites.
@@ -421,27 +462,27 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 // The narrowest groups of lanes that hold a row, four values a lane and load
 // where rows and pointers allow.  (Gradient of 4096 x 96: 4.2 us with 32 lanes a
 // row and four values a load, 5.9 with 64 and one.)
-#define MOE_ROW_SHAPE(E, vec4, CALL)        \
-  do {                                      \
-    if (vec4) {                             \
-      if ((E) <= 32) CALL(8, 1, 4);         \
-      else if ((E) <= 64) CALL(16, 1, 4);   \
-      else if ((E) <= 128) CALL(32, 1, 4);  \
-      else if ((E) <= 256) CALL(64, 1, 4);  \
-      else if ((E) <= 512) CALL(64, 2, 4);  \
-      else if ((E) <= 768) CALL(64, 3, 4);  \
-      else CALL(64, 4, 4);                  \
-    } else {                                \
-      if ((E) <= 8) CALL(8, 1, 1);          \
-      else if ((E) <= 16) CALL(16, 1, 1);   \
-      else if ((E) <= 32) CALL(32, 1, 1);   \
-      else if ((E) <= 64) CALL(64, 1, 1);   \
-      else if ((E) <= 128) CALL(64, 2, 1);  \
-      else if ((E) <= 256) CALL(64, 4, 1);  \
-      else if ((E) <= 512) CALL(64, 8, 1);  \
-      else if ((E) <= 768) CALL(64, 12, 1); \
-      else CALL(64, 16, 1);                 \
-    }                                       \
+#define MOE_ROW_SHAPE(E, vec4, CALL)            \
+  do {                                          \
+    if (vec4) {                                 \
+      if ((E) <= 32) { CALL(8, 1, 4); }         \
+      else if ((E) <= 64) { CALL(16, 1, 4); }   \
+      else if ((E) <= 128) { CALL(32, 1, 4); }  \
+      else if ((E) <= 256) { CALL(64, 1, 4); }  \
+      else if ((E) <= 512) { CALL(64, 2, 4); }  \
+      else if ((E) <= 768) { CALL(64, 3, 4); }  \
+      else { CALL(64, 4, 4); }                  \
+    } else {                                    \
+      if ((E) <= 8) { CALL(8, 1, 1); }          \
+      else if ((E) <= 16) { CALL(16, 1, 1); }   \
+      else if ((E) <= 32) { CALL(32, 1, 1); }   \
+      else if ((E) <= 64) { CALL(64, 1, 1); }   \
+      else if ((E) <= 128) { CALL(64, 2, 1); }  \
+      else if ((E) <= 256) { CALL(64, 4, 1); }  \
+      else if ((E) <= 512) { CALL(64, 8, 1); }  \
+      else if ((E) <= 768) { CALL(64, 12, 1); } \
+      else { CALL(64, 16, 1); }                 \
+    }                                           \
   } while (0)
 
 constexpr size_t kTicketBytes = 256;
@@ -459,6 +500,19 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const in
                                float* load, float* losses, void* ws, hipStream_t s) {
   unsigned* ticket = (unsigned*)ws;
   double* sums = (double*)((char*)ws + kTicketBytes);
+  // One launch for one sequence of so few rows that a block takes them in four
+  // turns (256 x 24: 16.2 us with the gradient, 19.6 in two launches).
+#define MOE_ALONE(W, N, VEC)                                                                   \
+  if (n_seq == 1 && (long long)T * W <= 4 * kLossThreads) {                                    \
+    MOE_LAUNCH("balance_alone", s,                                                             \
+               balance_alone<W, N, VEC><<<1, kLossThreads, 0, s>>>(                            \
+                   logits, idx, seq, group, T, E, K, balance_coef, z_coef, counts, tokens,     \
+                   load, losses));                                                             \
+    return hipGetLastError();                                                                  \
+  }
+  const bool vec4 = E % 4 == 0 && aligned16(logits) && aligned16(load);
+  MOE_ROW_SHAPE(E, vec4, MOE_ALONE);
+#undef MOE_ALONE
   // One launch where a block may count all picks and look at all tokens: 1024 picks
   // 3.3 us, where three launches take 4 and the host 5 more; 196608 picks 12 to 14
   // us, which three launches do in 10.
@@ -483,7 +537,7 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const in
                  <<<std::min(ceil_div(T, kLossThreads / W), kLossBlocks), kLossThreads, 0, s>>>( \
                      logits, seq, n_seq, T, E, load, tokens, balance_coef, z_coef, sums,       \
                      ticket, losses))
-  MOE_ROW_SHAPE(E, E % 4 == 0 && aligned16(logits) && aligned16(load), MOE_BALANCE);
+  MOE_ROW_SHAPE(E, vec4, MOE_BALANCE);
 #undef MOE_BALANCE
   return hipGetLastError();
 }
