@@ -8,7 +8,8 @@
 // the codes that are written, which the backward pass finds there of a smaller
 // batch, and the values that are converted alone, which another kernel has just
 // written (8192 x 2048 fp32 13.0 us so, 15.7 past the caches; 8192 x 6144 bf16
-// 28.4 and 27.3).
+// 28.4 and 27.3).  SwiGLU of 65387 rows of 2048 bf16 with its codes: 174 us each
+// way, 6.2 TB/s (187 with the default policy).
 #include "stream.h"
 #include "train_internal.h"
 

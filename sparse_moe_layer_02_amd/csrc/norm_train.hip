@@ -333,7 +333,8 @@ __global__ __launch_bounds__(THREADS) void layer_norm_kernel(
 // Up to 12288 values a row's threads have the weight in registers and the next
 // row's x and dy in flight while one is worked on: what a row costs once (its
 // sums, addresses) is shared by up to 24 values a lane, and the blocks of a CU
-// wait for different things.  Longer rows have neither.
+// wait for different things.  Longer rows have neither.  (8192 x 6144, bf16
+// gradients, fp32 stream: 115 us, 6.1 TB/s; bf16 from 8-bit rows 61 us, 5.8.)
 template <typename DY, typename X, typename DX, int P, int VEC, int THREADS, bool MEAN>
 __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward_kernel(
     Source<DY, VEC> dy, Source<X, VEC> x, const float* __restrict__ w, float eps, int rows, int H,
@@ -519,7 +520,8 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
     }
 }
 
-// d[h] = sum over n rows of sums[.][h], 64 columns a block; blockIdx.y: the
+// Eight loads in flight a thread (256 rows of 6144, weight and bias: 5 us; one at a
+// time 12).  d[h] = sum over n rows of sums[.][h], 64 columns a block; blockIdx.y: the
 // weight's sums, then the bias's, H floats behind them.
 constexpr int kJoinWaves = 16;
 __global__ __launch_bounds__(kWave* kJoinWaves) void join_sums(const float* __restrict__ sums,
