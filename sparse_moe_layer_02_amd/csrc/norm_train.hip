@@ -8,8 +8,8 @@
 // and the sums over it are taken there; the backward pass takes the row's
 // statistics again instead of reading them, from the x that it needs anyway.
 // Its blocks go over many rows each and keep the weights' gradients of their
-// rows in registers; the blocks' sums are joined by a second kernel in a fixed
-// order.
+// rows in registers, or in LDS on long rows; the blocks' sums are joined by a
+// second kernel in a fixed order.
 #include <type_traits>
 
 #include "norm_rows.h"
