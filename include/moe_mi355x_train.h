@@ -114,10 +114,11 @@ moe_status moe_norm_checkpoint(const void *x, int x_dtype, const float *weight, 
  *   y[t][h] = (x[t][h] - m[t]) / sqrt(v[t] + eps) * weight[h] + bias[h]
  * weight [H] fp32 or NULL (ones), bias [H] fp32 or NULL (zeros); codes and
  * scales: NULL, or x in 8 bits is left there as by moe_norm_checkpoint.  fp32
- * arithmetic, the deviations from the mean squared themselves; rows whose sums
- * or squares fp32 cannot hold are scaled by a power of two first.  A constant row
- * gives the bias with eps > 0, NaN with eps == 0.  y may be x when the dtypes
- * are equal.
+ * arithmetic, the deviations from the mean squared themselves and their own mean
+ * taken out of them again, so that a row far from zero keeps the digits that its
+ * values have of its spread; rows whose sums or squares fp32 cannot hold are
+ * scaled by a power of two first.  A constant row gives the bias with eps > 0,
+ * NaN with eps == 0.  y may be x when the dtypes are equal.
  * Errors as for moe_norm; with codes H % 32 == 0, and scales with codes. */
 moe_status moe_layer_norm(const void *x, int x_dtype, const float *weight, const float *bias,
                           float eps, int T, int H, void *y, int y_dtype, uint8_t *codes,

@@ -189,17 +189,29 @@ __global__ __launch_bounds__(kMaxThreads) void norm_checkpoint_kernel(
   }
 }
 
-// v = v - mean(v).
-template <int WAVES, int P, int VEC>
+// v = v - mean(v), but for the roundings of the mean's sum, which are not small
+// beside the deviations where a row is far from zero (nor zero where its values
+// are equal: 3 v is no fp32 number for most v).
+// over: divides a sum by the row's length, or multiplies it by the reciprocal, which
+// is a rounding more and saves a backward pass of 16384 x 2048 bf16 4 %.
+struct Length {
+  float h;
+  __device__ __forceinline__ float operator()(float sum) const { return sum / h; }
+};
+struct Reciprocal {
+  float inv;
+  __device__ __forceinline__ float operator()(float sum) const { return sum * inv; }
+};
+template <int WAVES, int P, int VEC, typename Over>
 __device__ __forceinline__ void center(float (&v)[P][VEC], const Pieces<P, VEC>& pieces,
-                                       int H, float (*part)[WAVES]) {
+                                       Over over, float (*part)[WAVES]) {
   float s[1] = {0.0f};
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) s[0] += v[p][i];
   row_sums<WAVES>(s, part);
-  const float m = s[0] / (float)H;   // exact where the row's values are equal
+  const float m = over(s[0]);
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -226,6 +238,49 @@ template <int P, int VEC> __device__ __forceinline__ void scale(float (&v)[P][VE
     for (int i = 0; i < VEC; ++i) v[p][i] *= f;
 }
 
+// What center() has left of the mean is alike for the whole row and of the
+// deviations' own size.  Their mean m, summed with their squares, is taken out of
+// the deviations where they are multiplied, and out of the squares' sum here.
+// (Without it rows of 6144 values of mean 1000 and spread 1 were off by 1e-4, and
+// equal values of 1000, which are normed to zeros, by up to 0.2.)  mostly: it is so
+// much of the squares that what stays of them may be roundings alone.
+struct Mean {
+  float m, ss;
+  bool mostly;
+};
+__device__ __forceinline__ Mean mean_left(float sum, float ss, float inv_h) {
+  const float m = sum * inv_h, of_mean = sum * m;
+  return {m, ss - of_mean, of_mean >= 0.0625f * ss && m != 0.0f};   // (both may be underflowed)
+}
+
+// Of the sum of squares as it was summed.
+__device__ __forceinline__ float scale_of_row(float ss, float eps) {
+  return too_large(ss) ? 0x1p-96f : too_small(ss, eps) ? 0x1p96f : 1.0f;
+}
+
+// The deviations of a row's values v, and the sum of their squares, where this left
+// fp32's range or the mean had most of it: rare, and the same for the row's
+// threads.  f: the power of two that they are scaled by, before the first mean is
+// taken where it is less than 1, behind it otherwise.  Three means, as the second has a
+// rounding of the first's error, which counts where the row is all but constant;
+// deviations of equal values have few digits, so that their sum is exact and they
+// become zeros, whose root is eps's alone: f's square would lose it.
+// part: 4 sums' LDS.
+template <int WAVES, int P, int VEC>
+__device__ __forceinline__ float deviations(float (&v)[P][VEC], const Pieces<P, VEC>& pieces,
+                                            int H, float& f, float (*part)[WAVES]) {
+  const bool large = f < 1.0f;
+  if (large) scale(v, f);
+#pragma unroll 1
+  for (int k = 0; k < 3; ++k) {
+    center(v, pieces, Length{(float)H}, part + k);
+    if (k == 0 && !large) scale(v, f);
+  }
+  const float ss = squares(v, part + 3);
+  if (large && ss == 0.0f) f = 1.0f;
+  return ss;
+}
+
 // SAVE: x in 8 bits to codes and scales too; the pieces of 32 / VEC neighbouring
 // threads are a block.  A block goes over the rows blockIdx.x * blockDim.y +
 // threadIdx.y, and so on; up to 12288 values its threads have weight and bias in
@@ -237,8 +292,9 @@ __global__ __launch_bounds__(THREADS) void layer_norm_kernel(
     int rows, int H, U* y, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   constexpr bool kAhead = THREADS <= 512;
   constexpr int kWaves = THREADS <= 256 ? 4 : 16;
-  __shared__ __attribute__((aligned(16))) float part[4][kWaves];
-  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 4 * kWaves;
+  constexpr int kSums = 7;
+  __shared__ __attribute__((aligned(16))) float part[kSums][kWaves];
+  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < kSums * kWaves;
        i += blockDim.x * blockDim.y)
     (&part[0][0])[i] = 0.0f;
   __syncthreads();
@@ -291,25 +347,29 @@ __global__ __launch_bounds__(THREADS) void layer_norm_kernel(
       }
     }
     pieces.clear_behind(v);
-    center(v, pieces, H, part);
-    float ss = squares(v, part + 1), f = 1.0f;
-    if (too_large(ss)) {
-      f = 0x1p-96f;
+    center(v, pieces, Reciprocal{inv_h}, part);
+    float s[2] = {0.0f, 0.0f};   // the deviations' squares, and themselves
 #pragma unroll
-      for (int p = 0; p < P; ++p) {   // the deviations may be lost already
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        s[0] = fmaf(v[p][i], v[p][i], s[0]);
+        s[1] += v[p][i];
+      }
+    row_sums<kWaves>(s, part + 1);
+    Mean left = mean_left(s[1], s[0], inv_h);
+    float f = scale_of_row(s[0], eps);
+    if (left.mostly || f != 1.0f) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
         const Raw again = x.load(row + pieces.at[p]);
         Source<T, VEC>::values(again, v[p]);
       }
       pieces.clear_behind(v);
-      scale(v, f);
-      center(v, pieces, H, part + 2);
-      ss = squares(v, part + 3);
-    } else if (too_small(ss, eps)) {
-      f = 0x1p96f;
-      scale(v, f);
-      ss = squares(v, part + 2);
+      left.ss = deviations(v, pieces, H, f, part + 3);
+      left.m = 0.0f;
     }
-    const float r = rsqrtf(ss * inv_h + eps * f * f);
+    const float r = rsqrtf(left.ss * inv_h + eps * f * f), mr = left.m * r;
     // the next row's loads end here, so that nothing waits for this row's stores
     if (kAhead) {
 #pragma unroll
@@ -321,7 +381,8 @@ __global__ __launch_bounds__(THREADS) void layer_norm_kernel(
       if (!kAhead) affine(p, g, c);
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        v[p][i] = fmaf(v[p][i] * r, kAhead ? weight[p][i] : g[i], kAhead ? bias[p][i] : c[i]);
+        v[p][i] = fmaf(fmaf(v[p][i], r, -mr), kAhead ? weight[p][i] : g[i],
+                       kAhead ? bias[p][i] : c[i]);
       if (pieces.inside(p)) store_past<VEC>(y + row + pieces.at[p], v[p]);
     }
   }
@@ -341,7 +402,7 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
     Source<DX, VEC> d_residual, DX* dx, float* __restrict__ sum_w, float* __restrict__ sum_b,
     int stride) {
   constexpr bool kAhead = THREADS <= 512;
-  constexpr int kSums = 9, kWaves = THREADS <= 256 ? 4 : 16;
+  constexpr int kSums = MEAN ? 13 : 5, kWaves = THREADS <= 256 ? 4 : 16;
   // the weights' gradients of a thread's columns: in registers, or, where these
   // do not hold them for two waves a SIMD, in LDS that is the thread's alone
   constexpr bool kInLds = kAhead && P * VEC > 16;
@@ -412,10 +473,10 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
     if (kAhead) fetch(t + step);
     pieces.clear_behind(v);
     pieces.clear_behind(d);
-    float s[3];
-    // the squares of v, g times v, and g
+    float s[4];
+    // the squares of v, g times v, g, and v
     const auto sums = [&](float (*lds)[kWaves]) {
-      s[0] = s[1] = s[2] = 0.0f;
+      s[0] = s[1] = s[2] = s[3] = 0.0f;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         float g[VEC];
@@ -425,7 +486,10 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
           const float gi = d[p][i] * (kAhead ? weight[p][i] : g[i]);
           s[0] = fmaf(v[p][i], v[p][i], s[0]);
           s[1] = fmaf(gi, v[p][i], s[1]);
-          if (MEAN) s[2] += gi;
+          if (MEAN) {
+            s[2] += gi;
+            s[3] += v[p][i];
+          }
         }
       }
       if (MEAN) {
@@ -437,29 +501,43 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
         s[1] = two[1];
       }
     };
-    if (MEAN) center(v, pieces, H, part[turn]);
-    sums(part[turn] + 1);
-    // n = v to_n, dx = (..) root f
-    float f = 1.0f, root = rsqrtf(s[0] * inv_h + eps), to_n = root;
-    if (too_large(s[0]) || too_small(s[0], eps) || !(fabsf(s[1]) < __builtin_inff())) {
+    float (*lds)[kWaves] = part[turn];
+    const auto own = [&](int n) {   // LDS of the next n sums
+      float (*at)[kWaves] = lds;
+      lds += n;
+      return at;
+    };
+    if (MEAN) center(v, pieces, Reciprocal{inv_h}, own(1));
+    sums(own(MEAN ? 4 : 2));
+    Mean left = {0.0f, s[0], false};
+    if (MEAN) {
+      left = mean_left(s[3], s[0], inv_h);
+      s[1] = fmaf(-left.m, s[2], s[1]);
+    }
+    // n = (v - m) to_n, dx = (..) root f
+    float f = scale_of_row(s[0], eps), root = rsqrtf(left.ss * inv_h + eps), to_n = root;
+    if (left.mostly || f != 1.0f || !(fabsf(s[1]) < __builtin_inff())) {
       // rare, and the same for the row's threads: v scaled, then normed before it meets g
-      const bool large = too_large(s[0]);
-      f = large ? 0x1p-96f : too_small(s[0], eps) ? 0x1p96f : 1.0f;
-      if (large) {   // the deviations may be lost already
 #pragma unroll
-        for (int p = 0; p < P; ++p) Source<X, VEC>::values(x.load(row + pieces.at[p]), v[p]);
-        pieces.clear_behind(v);
+      for (int p = 0; p < P; ++p) Source<X, VEC>::values(x.load(row + pieces.at[p]), v[p]);
+      pieces.clear_behind(v);
+      float ss;
+      if (MEAN) {
+        ss = deviations(v, pieces, H, f, own(4));
+        left.m = 0.0f;
+      } else {
+        scale(v, f);
+        ss = squares(v, own(1));
       }
-      scale(v, f);
-      if (MEAN && large) center(v, pieces, H, part[turn] + 4);
-      root = rsqrtf(squares(v, part[turn] + 5) * inv_h + eps * f * f);
+      root = rsqrtf(ss * inv_h + eps * f * f);
       scale(v, root);
       to_n = 1.0f;
-      sums(part[turn] + 6);
+      sums(own(MEAN ? 4 : 2));
     }
     // the next row's loads end here, so that nothing waits for this row's stores
     if (kAhead) arrived();
-    const float c = to_n * s[1] * inv_h, mean_g = MEAN ? s[2] * inv_h : 0.0f;
+    const float c = to_n * s[1] * inv_h, mean_g = MEAN ? s[2] * inv_h : 0.0f,
+                mn = left.m * to_n;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       float g[VEC], o[VEC] = {};
@@ -471,7 +549,8 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
       }
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float n = v[p][i] * to_n, gi = d[p][i] * (kAhead ? weight[p][i] : g[i]);
+        const float n = MEAN ? fmaf(v[p][i], to_n, -mn) : v[p][i] * to_n;
+        const float gi = d[p][i] * (kAhead ? weight[p][i] : g[i]);
         o[i] = fmaf((gi - mean_g - n * c) * root, f, o[i]);   // root f may pass 2^128
         dw[p][i] = fmaf(d[p][i], n, dw[p][i]);
         db[p][i] += d[p][i];
