@@ -538,6 +538,8 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
     if (kAhead) arrived();
     const float c = to_n * s[1] * inv_h, mean_g = MEAN ? s[2] * inv_h : 0.0f,
                 mn = left.m * to_n;
+    // f in two halves: neither root f nor (..) root is sure to be one of fp32's numbers
+    const float half = f < 1.0f ? 0x1p-48f : f > 1.0f ? 0x1p48f : 1.0f, root_half = root * half;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       float g[VEC], o[VEC] = {};
@@ -551,7 +553,7 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
       for (int i = 0; i < VEC; ++i) {
         const float n = MEAN ? fmaf(v[p][i], to_n, -mn) : v[p][i] * to_n;
         const float gi = d[p][i] * (kAhead ? weight[p][i] : g[i]);
-        o[i] = fmaf((gi - mean_g - n * c) * root, f, o[i]);   // root f may pass 2^128
+        o[i] = fmaf((gi - mean_g - n * c) * root_half, half, o[i]);
         dw[p][i] = fmaf(d[p][i], n, dw[p][i]);
         db[p][i] += d[p][i];
       }
