@@ -17,7 +17,7 @@ inline bool finite(float v) { return v == v && v - v == 0.0f; }
 inline moe_status launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 
 inline bool rows_ok(long long rows, int cols, int step) {
-  return rows >= 1 && cols >= 1 && cols % step == 0 && rows < (1ll << 34) / cols;
+  return rows >= 1 && cols >= 1 && cols % step == 0 && rows <= ((1ll << 34) - 1) / cols;
 }
 inline bool norm_ok(int T, int H, float eps, bool mx8) {
   return T >= 1 && H >= 1 && H % (mx8 ? 32 : 8) == 0 && H <= kMaxNorm && finite(eps) &&
