@@ -22,7 +22,7 @@ inline moe_status launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE
 
 // Sizes that the 4-bit rows of both conversions take.
 inline bool rows_ok(long long rows, int cols) {
-  return rows >= 1 && cols >= 1 && cols % 32 == 0 && rows < (1ll << 34) / cols;
+  return rows >= 1 && cols >= 1 && cols % 32 == 0 && rows <= ((1ll << 34) - 1) / cols;
 }
 
 // An expert's rows at most: with the dispatch indices one a token.

@@ -29,3 +29,12 @@ def test_swiglu_rows(I, kept):
     for rows, want in ((most, ALIGN), (most + 1, SHAPE)):
         assert lib.moe_swiglu(OFF, 1, rows, I, None, FAKE, s, s, None) == want, rows
         assert lib.moe_swiglu_backward(OFF, FAKE, s, 1, rows, I, None, FAKE, None, None) == want, rows
+
+
+@pytest.mark.parametrize("cols", [32, 96, 160, 2048, 6144, 12320, 1 << 20, (1 << 31) - 32])
+def test_mxfp4_rows(cols):
+    lib = moe.lib()
+    most = ((1 << 34) - 1) // cols
+    for rows, want in ((most, ALIGN), (most + 1, SHAPE)):
+        assert lib.moe_mxfp4_quantize(OFF, 1, rows, cols, None, FAKE, FAKE, None) == want, rows
+        assert lib.moe_mxfp4_dequantize(FAKE, FAKE, 0, rows, cols, OFF, None) == want, rows
