@@ -69,8 +69,10 @@ moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, const 
  * coefficients: as for moe_balance_loss; padding has a gradient from its
  * d_gate alone.  d_losses [2] fp32 in device memory: the gradients of the two
  * losses; NULL: ones.  d_logits [T][E] fp32; it may be logits.
- * A masked expert's gradient is 0, whatever d_gate holds for a pick of it (its
- * gate is 0), and so are those of a token whose logits are all -inf.  Errors as for moe_balance_loss; K is only looked at with d_gate. */
+ * A masked expert's gradient is 0, whatever d_gate and d_losses hold (its
+ * probability is 0), and so are those of a token whose logits are all -inf; a NaN
+ * or +inf in a token's logits makes all of its row NaN.
+ * Errors as for moe_balance_loss; K is only looked at with d_gate. */
 moe_status moe_route_backward(const float *logits, const int32_t *topk_idx, const float *d_gate,
                               const int32_t *seq, int n_seq, const int32_t *tokens,
                               const float *load, const float *d_losses, float balance_coef,

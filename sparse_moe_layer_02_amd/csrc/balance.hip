@@ -443,8 +443,8 @@ __global__ __launch_bounds__(kThreads) void route_backward(
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        if (p[i][j] == 0.0f) g[i][j] = 0.0f;   // a masked pick's gradient may be anything
         if (s >= 0) g[i][j] = fmaf(cb, f[i][j], g[i][j]);
+        if (p[i][j] == 0.0f) g[i][j] = 0.0f;   // a masked expert's may be anything
         dot = fmaf(p[i][j], g[i][j], dot);
       }
     dot = group_sum<W>(dot);
@@ -452,7 +452,8 @@ __global__ __launch_bounds__(kThreads) void route_backward(
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) p[i][j] *= g[i][j] - dot + more;
+      for (int j = 0; j < VEC; ++j)   // and so may the others' sum
+        p[i][j] = p[i][j] == 0.0f ? 0.0f : p[i][j] * (g[i][j] - dot + more);
     Row::store(d_logits + t * E, E, l, p);
   }
 }
