@@ -96,8 +96,9 @@ moe_status moe_mxfp8_quantize(const void *x, int dtype, long long rows, int cols
 
 /* The values that MXFP8 rows stand for, in dtype: exact in fp32; in bf16 too,
  * but for magnitudes below 2^-126, which are rounded (only blocks at the lowest
- * scales hold such values).  Magnitudes of 2^128 and more become infinities
- * (moe_mxfp8_quantize makes none).
+ * scales hold such values).  Magnitudes of 2^128 and more become infinities:
+ * moe_mxfp8_quantize rounds finite ones from 1.9375 * 2^127 on to 2^128 (256 at
+ * scale 2^120), and passes that read a checkpoint have infinities in their place.
  * y [rows][cols] (16-byte aligned); the rest as for moe_mxfp8_quantize. */
 moe_status moe_mxfp8_dequantize(const uint8_t *codes, const uint8_t *scales, int dtype,
                                 long long rows, int cols, void *y, void *stream);

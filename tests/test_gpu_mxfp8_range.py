@@ -1,0 +1,55 @@
+"""What MXFP8 promises of its values: which of them become infinities, and how far the others are off."""
+import numpy as np
+import pytest
+import torch
+
+import _train as ref
+import sparse_moe_layer_02_amd as moe
+from _parity import device
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _there_and_back(x, library):
+    """The values that x comes back as, by the 64-bit form; the library's have to be the same."""
+    codes, scales = ref.mx8_quantize(x.double().numpy())
+    v = ref.mx8_values(codes, scales)
+    if library:
+        d = x.to(device())
+        kept = moe.alloc_checkpoint(x.shape)
+        moe.moe_mxfp8_quantize(d, *kept)
+        y = torch.empty_like(d)
+        moe.moe_mxfp8_dequantize(*kept, y)
+        assert np.array_equal(kept.codes.cpu().numpy(), codes) and np.array_equal(kept.scales.cpu().numpy(), scales)
+        want = np.where(np.abs(v) < 2.0 ** 128, v, np.copysign(np.inf, v))
+        assert np.array_equal(ref.f64(y), want)
+    return v
+
+
+def _largest(dtype):
+    top = torch.finfo(dtype).max
+    x = torch.tensor([1.9375, 1.9296875, 1.75, 1.7578125, 1.0, 0.25] * 5 + [0.0, 0.0], dtype=torch.float64) * 2.0 ** 127
+    x = torch.stack([torch.full((32,), top, dtype=torch.float64), x, x * 0.875, -x, -torch.full((32,), top, dtype=torch.float64)])
+    x[:, 31] = -x[:, 0] * 0.5
+    return x.to(dtype)
+
+
+def _check_largest(dtype, library):
+    x = _largest(dtype)
+    v, a = _there_and_back(x, library), x.double().numpy()
+    far = np.abs(a) >= 1.9375 * 2.0 ** 127
+    assert far[0, 0] and far[1, 0] and not far[1, 1]
+    assert (np.abs(v[far]) == 2.0 ** 128).all() and (np.abs(v[~far]) < 2.0 ** 128).all()
+    assert (np.abs(v - a) <= np.abs(a) / 16).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_largest_values_by_definition(dtype):
+    _check_largest(dtype, False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_largest_values(dtype):
+    """Finite values from 1.9375 * 2^127 on come back as infinities, no others."""
+    _check_largest(dtype, True)
