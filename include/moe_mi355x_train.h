@@ -81,9 +81,10 @@ moe_status moe_route_backward(const float *logits, const int32_t *topk_idx, cons
 /* Rows to MXFP8.  For each block of 32 values x_i with m = max |x_i|:
  *   scale  = the smallest power of two with m / scale <= 448, at least 2^-127
  *   code_i = x_i / scale rounded to e4m3, ties to the even code
- * so no value is clipped, and one within a factor of 2^14 of its block's
- * largest is off by at most 2^-4 of itself.  A block that holds a NaN or an
- * infinity gets scale byte 255 and NaN codes.
+ * so no value is clipped.  In a block whose scale is above 2^-127 the largest is
+ * more than 224 scales, and a value within a factor of 7 * 2^11 of it, so of 2^-6
+ * scales or more (e4m3's normal numbers), is off by at most 2^-4 of itself.  A
+ * block that holds a NaN or an infinity gets scale byte 255 and NaN codes.
  *   x [rows][cols] (dtype, 16-byte aligned), codes [rows][cols] (16-byte
  *   aligned), scales [rows][cols / 32] (4-byte aligned).
  * n_rows: NULL, or one int32 in device memory: only the first

@@ -53,3 +53,33 @@ def test_largest_values_by_definition(dtype):
 def test_largest_values(dtype):
     """Finite values from 1.9375 * 2^127 on come back as infinities, no others."""
     _check_largest(dtype, True)
+
+
+def _check_error(library):
+    rng = np.random.default_rng(0)
+    rows = []
+    for scale in (2.0 ** -126, 2.0 ** -60, 1.0, 2.0 ** 90):
+        for top in (np.nextafter(np.float32(224), np.float32(225)), np.float32(225.5), np.float32(300), np.float32(448)):
+            ratio = np.exp2(rng.uniform(0, np.log2(7 * 2.0 ** 11), (200, 32)))
+            ratio[:, 0], ratio[:, 1] = 1.0, 7 * 2.0 ** 11
+            rows.append(np.float64(top) * scale / ratio)
+    x = torch.as_tensor(np.concatenate(rows)).to(F32)
+    a = x.double().numpy()
+    inside = np.abs(a) * (7 * 2.0 ** 11) >= np.abs(a).max(1, keepdims=True)
+    assert inside.mean() > 0.9
+    v = _there_and_back(x, library)
+    assert (np.abs(v - a) <= np.abs(a) / 16)[inside].all()
+
+
+def test_error_by_definition():
+    _check_error(False)
+    x = np.full((1, 32), 224.5)                      # 2^14 is too far
+    x[0, 1] = 7.5 / 512
+    v = ref.mx8_values(*ref.mx8_quantize(x))
+    assert abs(v[0, 1] - x[0, 1]) > x[0, 1] / 16 and x[0, 0] / x[0, 1] < 2.0 ** 14
+
+
+@pytest.mark.gpu
+def test_error():
+    """Values within a factor of 7 * 2^11 of their block's largest are off by at most 2^-4."""
+    _check_error(True)
