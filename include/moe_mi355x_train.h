@@ -48,8 +48,8 @@ extern "C" {
  * logits makes the losses NaN.  N == 0: both losses 0.
  * fp32 softmax, the sums over tokens in fp64.
  * MOE_ERR_SHAPE: T < 1, K outside 1..E, E > 1024, T*E or T*K >= 2^31, n_seq
- * outside 1..65536 or not 1 without seq, n_seq*E >= 2^31, a coefficient that is
- * not finite.  MOE_ERR_ALIGN: pointers 4 bytes, ws 256.
+ * outside 1..65536 or not 1 without seq, a coefficient that is not finite.
+ * MOE_ERR_ALIGN: pointers 4 bytes, ws 256.
  * ws: at least moe_balance_loss_workspace_bytes(T, E, n_seq). */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int n_seq);
 moe_status moe_balance_loss(const float *logits, const int32_t *topk_idx, const int32_t *seq,

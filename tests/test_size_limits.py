@@ -38,3 +38,11 @@ def test_mxfp4_rows(cols):
     for rows, want in ((most, ALIGN), (most + 1, SHAPE)):
         assert lib.moe_mxfp4_quantize(OFF, 1, rows, cols, None, FAKE, FAKE, None) == want, rows
         assert lib.moe_mxfp4_dequantize(FAKE, FAKE, 0, rows, cols, OFF, None) == want, rows
+
+
+def test_most_sequences_and_experts():
+    f, F = moe.lib().moe_balance_loss, ctypes.c_float
+    need = moe.lib().moe_balance_loss_workspace_bytes(64, 1024, 65536)
+    # logits, idx, seq, n_seq, group, T, E, K, bc, zc, counts, tokens, load, losses, ws, bytes
+    for n_seq, E, want in ((65536, 1024, ALIGN), (65537, 1024, SHAPE), (65536, 1025, SHAPE)):
+        assert f(OFF, FAKE, FAKE, n_seq, FAKE, 64, E, 4, F(1.0), F(0.0), FAKE, FAKE, FAKE, FAKE, FAKE, need, None) == want
