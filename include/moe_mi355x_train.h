@@ -167,7 +167,8 @@ moe_status moe_layer_norm_backward(const void *dy, int dy_dtype, const void *x, 
  * gu [rows][2I] (dtype), hh [rows][I] (dtype); codes [rows][2I] and scales
  * [rows][2I / 32]: NULL, or gu in 8 bits as by moe_mxfp8_quantize.
  * n_rows as for moe_mxfp8_quantize (offsets + n_ffn takes the grouped rows).
- * fp32 arithmetic, rounded once.
+ * fp32 arithmetic, rounded once; where exp(-a) passes 2^128 (a below -88.7, silu
+ * above -3e-37) the output is 0.
  * MOE_ERR_SHAPE: rows < 1, I < 1, I % 8 (with codes I % 32) or rows * 2I >=
  * 2^34.  MOE_ERR_ALIGN: 16 bytes, scales and n_rows 4. */
 moe_status moe_swiglu(const void *gu, int dtype, long long rows, int I, const int32_t *n_rows,

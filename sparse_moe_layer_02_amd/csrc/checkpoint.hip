@@ -73,8 +73,9 @@ __global__ __launch_bounds__(kThreads) void mxfp8_dequantize(Source<Mx8, piece_o
   }
 }
 
-// In fp32 to the last digits, in bf16 to a good deal more than it holds.
-template <typename T> __device__ __forceinline__ float sigmoid(float g) {
+// One form for both types, off by the few steps of exp, sum and quotient, which the
+// sweeps hide behind memory: 0 from where exp(-g) passes 2^128, gates below -88.7.
+__device__ __forceinline__ float sigmoid(float g) {
   return 1.0f / (1.0f + expf(-g));
 }
 
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(Source<T, piece_of<T>(
       Source<T, VEC>::values(raw_g, g);
       Source<T, VEC>::values(raw_u, w);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) h[k] = g[k] * sigmoid<T>(g[k]) * w[k];
+      for (int k = 0; k < VEC; ++k) h[k] = g[k] * sigmoid(g[k]) * w[k];
       store_past<VEC>(hh + i * VEC, h);
       if (SAVE) {
         store_codes<VEC>(g, at, codes, scales);
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
       Source<X, VEC>::values(raw_u, w);
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        const float s = sigmoid<T>(g[k]), a = g[k] * s, dk = d[k];
+        const float s = sigmoid(g[k]), a = g[k] * s, dk = d[k];
         h[k] = a * w[k];
         d[k] = dk * w[k] * (s + a * (1.0f - s));
         w[k] = dk * a;
