@@ -58,8 +58,8 @@ __device__ __forceinline__ void loads_of(int s, int picks, int g, bool grouped, 
 
 // Counts and loads of sequence s by a block, which looks at all tokens'
 // sequences, 64 tokens to a wave, and counts the picks of those of its own in LDS.
-constexpr int kLook = 16;   // windows of 64 tokens whose sequences a wave has in flight
-constexpr int kPicks = 12;  // picks that a lane has in flight
+constexpr int kPicks = 12;  // picks that a lane has in flight (2730 x 768, K 12: 15.9 us the
+                            // losses so, 19.6 with one, 16.5 with 4, 17.5 with 24)
 struct CountLds {
   int hist[kMaxRouteE], sum[kMaxRouteE], size[kMaxRouteE];
   int mine, all;
@@ -74,33 +74,24 @@ __device__ __forceinline__ void count_sequence(int s, CountLds& lds, const int32
   if (threadIdx.x == 0) lds.mine = lds.all = 0;
   __syncthreads();
   int n = 0, inside = 0;
-  for (int t0 = threadIdx.x / kWave * kWave; t0 < T; t0 += kLook * kCountThreads) {
-    int q[kLook];
+  for (int t0 = threadIdx.x / kWave * kWave; t0 < T; t0 += kCountThreads) {
+    const int q = t0 + lane < T ? sequence(seq, n_seq, t0 + lane) : -1;
+    const uint64_t here = __ballot(q == s);
+    inside += __popcll(__ballot(q >= 0));
+    n += __popcll(here);
+    if (here == 0) continue;
+    const int32_t* picks = idx + (size_t)t0 * K;
+    // bits of tokens past T are not set: their picks are not read
+    for (int i0 = lane; i0 < kWave * K; i0 += kPicks * kWave) {
+      int e[kPicks];
 #pragma unroll
-    for (int u = 0; u < kLook; ++u) {
-      const int t = t0 + u * kCountThreads + lane;
-      q[u] = t < T ? sequence(seq, n_seq, t) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < kLook; ++u) {
-      if (t0 + u * kCountThreads >= T) break;
-      const uint64_t here = __ballot(q[u] == s);
-      inside += __popcll(__ballot(q[u] >= 0));
-      n += __popcll(here);
-      if (here == 0) continue;
-      const int32_t* picks = idx + (size_t)(t0 + u * kCountThreads) * K;
-      // bits of tokens past T are not set: their picks are not read
-      for (int i0 = lane; i0 < kWave * K; i0 += kPicks * kWave) {
-        int e[kPicks];
-#pragma unroll
-        for (int k = 0; k < kPicks; ++k) {
-          const int i = i0 + k * kWave;
-          e[k] = i < kWave * K && (here >> (i / K) & 1) ? picks[i] : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < kPicks; ++k)
-          if (e[k] >= 0 && e[k] < E) atomicAdd(&lds.hist[e[k]], 1);
+      for (int k = 0; k < kPicks; ++k) {
+        const int i = i0 + k * kWave;
+        e[k] = i < kWave * K && (here >> (i / K) & 1) ? picks[i] : -1;
       }
+#pragma unroll
+      for (int k = 0; k < kPicks; ++k)
+        if (e[k] >= 0 && e[k] < E) atomicAdd(&lds.hist[e[k]], 1);
     }
   }
   if (lane == 0) {
@@ -487,7 +478,7 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
   } while (0)
 
 constexpr size_t kTicketBytes = 256;
-constexpr long long kSequencePicks = 32768, kSequenceTokens = 1 << 20;
+constexpr long long kSequencePicks = 32768, kSequenceTokens = 1 << 22;
 
 }  // namespace
 
@@ -502,7 +493,8 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const in
   unsigned* ticket = (unsigned*)ws;
   double* sums = (double*)((char*)ws + kTicketBytes);
   // One launch for one sequence of so few rows that a block takes them in four
-  // turns (256 x 24: 16.2 us with the gradient, 19.6 in two launches).
+  // turns (24, 96 and 768 experts: 7.9, 8.0 and 9.8 us at four, 9.3, 10.2 and 15.1 at
+  // eight; in two launches 10.8 at either).
 #define MOE_ALONE(W, N, VEC)                                                                   \
   if (n_seq == 1 && (long long)T * W <= 4 * kLossThreads) {                                    \
     MOE_LAUNCH("balance_alone", s,                                                             \
@@ -514,9 +506,11 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const in
   const bool vec4 = E % 4 == 0 && aligned16(logits) && aligned16(load);
   MOE_ROW_SHAPE(E, vec4, MOE_ALONE);
 #undef MOE_ALONE
-  // One launch where a block may count all picks and look at all tokens: 1024 picks
-  // 3.3 us, where three launches take 4 and the host 5 more; 196608 picks 12 to 14
-  // us, which three launches do in 10.
+  // One launch where a block may count all picks and look at all tokens of every
+  // sequence.  The losses in us, so and with three launches: 32768 picks 16.0 and 17.1
+  // of one sequence, 11.6 and 17.4 of 16; 49152 picks 20.7 and 16.8, 15.1 and 17.2.
+  // 32768 picks, 2^22 looks 15.3 and 18.9 (K 8) and 15.9 and 31.1 (K 2), 2^24 32.3 and
+  // 20.5, 22.9 and 20.7.
   if ((long long)T * K <= kSequencePicks && (long long)T * n_seq <= kSequenceTokens) {
     MOE_LAUNCH("balance_count", s,
                balance_count_sequence<<<n_seq, kCountThreads, 0, s>>>(

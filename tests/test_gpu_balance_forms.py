@@ -100,8 +100,9 @@ def test_losses_of_any_pool(E, n):
     _check_loss(logits, idx, seq, n)
 
 
-@pytest.mark.parametrize("T,K,n", [(2730, 12, 1), (2731, 12, 1), (1024, 32, 9), (1025, 32, 9), (16384, 2, 64), (16384, 2, 65)])
+@pytest.mark.parametrize("T,K,n", [(2730, 12, 1), (2731, 12, 1), (1024, 32, 9), (1025, 32, 9), (16384, 2, 64), (16384, 2, 65),
+                                   (16384, 2, 256), (16384, 2, 257), (4096, 8, 1024), (4096, 8, 1025)])
 def test_both_sides_of_the_count_in_one_launch(T, K, n):
-    """2^15 picks and 2^20 looks at a token's sequence, and the next more of either."""
+    """2^15 picks and 2^22 looks at a token's sequence, and the next more of either."""
     logits, idx, seq = _case(T, 48, K, n, order="mixed")
     _check_loss(logits, idx, seq, n)
