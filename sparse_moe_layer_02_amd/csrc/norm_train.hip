@@ -514,8 +514,9 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
       left = mean_left(s[3], s[0], inv_h);
       s[1] = fmaf(-left.m, s[2], s[1]);
     }
-    // n = (v - m) to_n, dx = (..) root f
+    // n = (v - m) to_n, dx = (..) root half
     float f = scale_of_row(s[0], eps), root = rsqrtf(left.ss * inv_h + eps), to_n = root;
+    float half = 1.0f;
     if (left.mostly || f != 1.0f || !(fabsf(s[1]) < __builtin_inff())) {
       // rare, and the same for the row's threads: v scaled, then normed before it meets g
 #pragma unroll
@@ -533,13 +534,14 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
       scale(v, root);
       to_n = 1.0f;
       sums(own(MEAN ? 4 : 2));
+      // f in two halves: neither root f nor (..) root is sure to be one of fp32's numbers
+      half = f < 1.0f ? 0x1p-48f : f > 1.0f ? 0x1p48f : 1.0f;
+      root *= half;
     }
     // the next row's loads end here, so that nothing waits for this row's stores
     if (kAhead) arrived();
     const float c = to_n * s[1] * inv_h, mean_g = MEAN ? s[2] * inv_h : 0.0f,
                 mn = left.m * to_n;
-    // f in two halves: neither root f nor (..) root is sure to be one of fp32's numbers
-    const float half = f < 1.0f ? 0x1p-48f : f > 1.0f ? 0x1p48f : 1.0f, root_half = root * half;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       float g[VEC], o[VEC] = {};
@@ -553,7 +555,7 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward
       for (int i = 0; i < VEC; ++i) {
         const float n = MEAN ? fmaf(v[p][i], to_n, -mn) : v[p][i] * to_n;
         const float gi = d[p][i] * (kAhead ? weight[p][i] : g[i]);
-        o[i] = fmaf((gi - mean_g - n * c) * root_half, half, o[i]);
+        o[i] = fmaf((gi - mean_g - n * c) * root, half, o[i]);
         dw[p][i] = fmaf(d[p][i], n, dw[p][i]);
         db[p][i] += d[p][i];
       }
