@@ -190,8 +190,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_checkpoint_kernel(
 }
 
 // v = v - mean(v), but for the roundings of the mean's sum, which are not small
-// beside the deviations where a row is far from zero (nor zero where its values
-// are equal: 3 v is no fp32 number for most v).
+// beside the deviations where a row is far from zero (nor none where its values are
+// equal: 3 v is no fp32 number for most v).
 // over: divides a sum by the row's length, or multiplies it by the reciprocal, which
 // is a rounding more and saves a backward pass of 16384 x 2048 bf16 4 %.
 struct Length {
@@ -394,8 +394,9 @@ __global__ __launch_bounds__(THREADS) void layer_norm_kernel(
 // Up to 12288 values a row's threads have the weight in registers and the next
 // row's x and dy in flight while one is worked on: what a row costs once (its
 // sums, addresses) is shared by up to 24 values a lane, and the blocks of a CU
-// wait for different things.  Longer rows have neither.  (8192 x 6144, bf16
-// gradients, fp32 stream: 115 us, 6.1 TB/s; bf16 from 8-bit rows 61 us, 5.8.)
+// wait for different things.  (8192 x 6144, bf16 gradients, fp32 stream: 115 us,
+// 6.1 TB/s; bf16 from 8-bit rows 62 us, 5.7.)  Longer rows have neither, and their 32
+// values a lane do not fit 128 registers (2048 x 16384: 268 us, 1.8 TB/s).
 template <typename DY, typename X, typename DX, int P, int VEC, int THREADS, bool MEAN>
 __global__ __launch_bounds__(THREADS, THREADS <= 512 ? 2 : 1) void norm_backward_kernel(
     Source<DY, VEC> dy, Source<X, VEC> x, const float* __restrict__ w, float eps, int rows, int H,
